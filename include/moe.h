@@ -279,6 +279,97 @@ int64_t moe_ep_recv_capacity(const moe_ep_handle* handle);
 void moe_ep_destroy(moe_ep_handle* handle);
 
 /* ---------------------------------------------------------------------------------
+ * Products grouped by expert over ragged rows, for experts that are not this library's
+ * SwiGLU (or that train with their own steps in between): expert e owns counts[e]
+ * consecutive rows, experts in order and unpadded -- the form in which moe_ep_dispatch
+ * returns send_rows and expert_counts.  ("Top-k routing, from affinities to gates": the
+ * tokens of each expert are grouped and each expert runs one dense product over its rows.)
+ *   moe_grouped_mm        y[r, :]  = x[r, :] W_e^T
+ *   moe_grouped_mm_dgrad  dx[r, :] = dy[r, :] W_e
+ *   moe_grouped_mm_wgrad  dw_e     = dy_e^T x_e (fp32; 0 for an expert without rows), or
+ *                         dw_e    += dy_e^T x_e with accumulate != 0
+ * x, dx [rows, k]; y, dy [rows, n]; w [n_groups, n, k]; dw [n_groups, n, k] fp32; the rest in
+ * dtype (MOE_BF16 or MOE_FP32), products accumulated in fp32 and rounded once.
+ * counts [n_groups] int32; all pointers DEVICE.  rows is the buffers' capacity: rows behind
+ * the last expert's are not read into any result and not written; a negative count counts as
+ * 0, and rows that counts claims past `rows` are ignored.  1 <= n_groups <= 1024, rows < 2^30
+ * (0 allowed), any n and k up to 2^20; bf16 products with n and k multiples of 8 and 16-byte
+ * aligned buffers run on the tensor cores, others on the CUDA cores.  An output may not
+ * overlap an input.  No workspace, no allocation, no host synchronisation; deterministic.
+ * Each result depends only on its own expert's rows (infinities and NaNs of other rows do
+ * not reach it).  */
+moe_status moe_grouped_mm(const void* x, const void* w, const int32_t* counts, int32_t n_groups,
+                          int64_t rows, int32_t n, int32_t k, int32_t dtype, void* y,
+                          moe_stream_t stream);
+moe_status moe_grouped_mm_dgrad(const void* dy, const void* w, const int32_t* counts,
+                                int32_t n_groups, int64_t rows, int32_t n, int32_t k, int32_t dtype,
+                                void* dx, moe_stream_t stream);
+moe_status moe_grouped_mm_wgrad(const void* dy, const void* x, const int32_t* counts,
+                                int32_t n_groups, int64_t rows, int32_t n, int32_t k, int32_t dtype,
+                                int32_t accumulate, float* dw, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * The norms before and after a block, fused with its gate, the residual scale and the
+ * residual add.  (The pages leave the norms out of their equations; a block of a trained
+ * model is r = x + FFN(norm(x)).)  Per row, s(v) = 1 / sqrt(mean(v^2) + eps):
+ *   r = beta x + gate p,   p = y s(y) post_weight, or y without post_weight
+ *   u = r s(r) pre_weight  (from r before it is rounded to dtype)
+ * x [T, d] the residual stream, y [T, d] the block's output, u the next block's input; x, y,
+ * r, u in dtype (MOE_BF16 or MOE_FP32), the rest fp32: gate [d] (MOE_GATE_CHANNEL), [T]
+ * (MOE_GATE_TOKEN) or NULL (MOE_GATE_NONE: 1), post_weight, pre_weight [d], the statistics
+ * post_rstd = s(y), pre_rstd = s(r) [T].  NULL: y, with r, gate and post_weight (then r is x,
+ * beta must be 1 and only u is computed); post_weight with post_rstd (no norm after the
+ * block); pre_weight with u and pre_rstd (no norm before the next).
+ * Backward, from dr and du, the gradients of r and u (dr may be NULL -- zero -- when
+ * pre_weight is given): dx, dy in dtype; d_gate ([d] or [T]), d_post_weight, d_pre_weight
+ * fp32, each given exactly when its parameter is.  r, post_rstd and pre_rstd are the
+ * forward's; without y, dx is the gradient of x = r.  workspace: 16-byte aligned DEVICE
+ * memory of moe_block_norm_workspace(T, d) bytes, free again when the call's work is done.
+ * 0 <= T < 2^31, 1 <= d <= 16384, eps > 0.  r and u may each be x or y itself (not both the
+ * same one), dx and dy each one of y, r, dr, du; other overlaps are refused.  No allocation,
+ * no host synchronisation; deterministic (fixed-order sums, no atomics). */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_gate_kind;
+moe_status moe_block_norm(const void* x, const void* y, const float* gate, int32_t gate_kind,
+                          const float* post_weight, const float* pre_weight, int64_t T, int32_t d,
+                          int32_t dtype, float beta, float eps, void* r, void* u,
+                          float* post_rstd, float* pre_rstd, moe_stream_t stream);
+size_t moe_block_norm_workspace(int64_t T, int32_t d);
+moe_status moe_block_norm_backward(const void* y, const void* r, const void* dr, const void* du,
+                                   const float* gate, int32_t gate_kind, const float* post_weight,
+                                   const float* pre_weight, const float* post_rstd,
+                                   const float* pre_rstd, int64_t T, int32_t d, int32_t dtype,
+                                   float beta, void* dx, void* dy, float* d_gate,
+                                   float* d_post_weight, float* d_pre_weight, void* workspace,
+                                   size_t workspace_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * The global 2-norm of many gradient tensors, and clipping to a given norm (for the
+ * gradients of moe_backward and any others):
+ *   N = sqrt(sum over all tensors of g^2),   out = g * min(1, max_norm / N)
+ * grads, outs, numels, dtypes: HOST arrays of n_tensors entries -- DEVICE pointers (aligned to
+ * their type), element counts (0 allowed), MOE_FP32 or MOE_BF16 each; they are read during
+ * the call only.  outs[i] is grads[i] itself (in place) or a buffer that overlaps none of the
+ * others; the same buffer twice among the outputs is refused.  Squares and sums are 64-bit,
+ * in an order fixed by the sizes.  When N <= max_norm, or N is not finite, the coefficient is
+ * 1: gradients in place stay untouched, and the caller sees N.  workspace: 8-byte aligned
+ * DEVICE memory of moe_grad_workspace(n_tensors) bytes, free again when the call's work is done.
+ *   moe_clip_grad_norm  both steps; norm [1] fp32 (DEVICE) = N
+ *   moe_grad_sumsq      sum of g^2 to sumsq [1] (fp64) and/or its root to norm [1] (fp32)
+ *   moe_grad_scale      the second step for a given sumsq [1] (e.g. summed over ranks whose
+ *                       gradients are parts of one model's); norm may be NULL
+ * No allocation, no host synchronisation. */
+size_t moe_grad_workspace(int32_t n_tensors);
+moe_status moe_grad_sumsq(const void* const* grads, const int64_t* numels, const int32_t* dtypes,
+                          int32_t n_tensors, double* sumsq, float* norm, void* workspace,
+                          size_t workspace_bytes, moe_stream_t stream);
+moe_status moe_grad_scale(const void* const* grads, void* const* outs, const int64_t* numels,
+                          const int32_t* dtypes, int32_t n_tensors, const double* sumsq,
+                          float max_norm, float* norm, moe_stream_t stream);
+moe_status moe_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,
+                              const int32_t* dtypes, int32_t n_tensors, float max_norm, float* norm,
+                              void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
  * Allocation-free router step.  (The DeepSeekMoE pages have no counterpart: this is a
  * deployment convenience of this library.)
  *

@@ -33,7 +33,7 @@ class MoeError(RuntimeError):
 
 _lib = None
 
-_P = ctypes.c_void_p
+_P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 _SIGS = {
     "moe_create": (ctypes.c_int, [ctypes.POINTER(MoeCfg), ctypes.POINTER(ctypes.c_void_p)]),
     "moe_forward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P]),
@@ -64,6 +64,20 @@ _SIGS = {
     "moe_backward_prepare": (ctypes.c_int, [_P]),
     "moe_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P,
                                     _P]),
+    "moe_grouped_mm": (ctypes.c_int, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _P, _P]),
+    "moe_grouped_mm_dgrad": (ctypes.c_int, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _P, _P]),
+    "moe_grouped_mm_wgrad": (ctypes.c_int, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _I32, _P, _P]),
+    "moe_block_norm": (ctypes.c_int, [_P, _P, _P, _I32, _P, _P, _I64, _I32, _I32, ctypes.c_float,
+                                      ctypes.c_float, _P, _P, _P, _P, _P]),
+    "moe_block_norm_workspace": (ctypes.c_size_t, [_I64, _I32]),
+    "moe_block_norm_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _I64, _I32,
+                                               _I32, ctypes.c_float, _P, _P, _P, _P, _P, _P,
+                                               ctypes.c_size_t, _P]),
+    "moe_grad_workspace": (ctypes.c_size_t, [_I32]),
+    "moe_grad_sumsq": (ctypes.c_int, [_P, _P, _P, _I32, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_grad_scale": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, ctypes.c_float, _P, _P]),
+    "moe_clip_grad_norm": (ctypes.c_int, [_P, _P, _P, _P, _I32, ctypes.c_float, _P, _P,
+                                          ctypes.c_size_t, _P]),
     "moe_kernels_per_forward": (ctypes.c_int32, [_P]),
     "moe_device_bytes": (ctypes.c_size_t, [_P]),
     "moe_destroy": (None, [_P]),

@@ -1,0 +1,126 @@
+"""The norms before and after a block, fused with its gate, the residual scale and the
+residual add (moe_block_norm* in include/moe.h), forward and backward.
+
+Per row, s(v) = 1 / sqrt(mean(v^2) + eps):
+  r = beta x + gate p,  p = y s(y) post_weight   (p = y without post_weight)
+  u = r s(r) pre_weight                          (the next block's input)
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from ._call import DTYPES, check_tensor, on_stream, rows_of
+from ._lib import check, lib
+from .layer import _ptr
+
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
+
+
+class BlockNorm(NamedTuple):
+    r: torch.Tensor                  # [T, d] the residual stream after the block
+    u: torch.Tensor | None           # [T, d] the next block's input (pre_weight given)
+    post_rstd: torch.Tensor | None   # [T] fp32 (post_weight given)
+    pre_rstd: torch.Tensor | None    # [T] fp32 (pre_weight given)
+
+
+class BlockNormGrads(NamedTuple):
+    dx: torch.Tensor                     # [T, d]
+    dy: torch.Tensor | None              # [T, d] (y given)
+    d_gate: torch.Tensor | None          # fp32, the gate's shape
+    d_post_weight: torch.Tensor | None   # [d] fp32
+    d_pre_weight: torch.Tensor | None    # [d] fp32
+
+
+def _params(dev, rows, d, gate, post_weight, pre_weight) -> int:
+    """Check the parameters; the gate's kind."""
+    kind = GATE_NONE
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor):
+            raise ValueError("gate must be a tensor")
+        kind = GATE_TOKEN if gate.dim() == 2 else GATE_CHANNEL
+        check_tensor("gate (one value per channel [d], or per token [T, 1])", gate, dev,
+                     (rows, 1) if kind == GATE_TOKEN else (d,), torch.float32)
+    if post_weight is not None:
+        check_tensor("post_weight", post_weight, dev, (d,), torch.float32)
+    if pre_weight is not None:
+        check_tensor("pre_weight", pre_weight, dev, (d,), torch.float32)
+    return kind
+
+
+def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, gate: torch.Tensor | None = None,
+               post_weight: torch.Tensor | None = None, pre_weight: torch.Tensor | None = None,
+               beta: float = 1.0, eps: float = 1e-6, out: BlockNorm | None = None,
+               stream: torch.cuda.Stream | None = None) -> BlockNorm:
+    """The step between two blocks.  x [T, d] the residual stream, y [T, d] the block's output
+    (None: only the norm before the first block, r is x itself); gate fp32 [d] per channel or
+    [T, 1] per token; weights fp32 [d].  `out` may reuse x or y as r or u."""
+    dev, rows, d, dt = rows_of("x", x)
+    if y is not None:
+        check_tensor("y", y, dev, (rows, d), dt)
+    kind = _params(dev, rows, d, gate, post_weight, pre_weight)
+    if out is not None:
+        if (out.u is not None) != (pre_weight is not None) or \
+                (out.pre_rstd is not None) != (pre_weight is not None) or \
+                (out.post_rstd is not None) != (post_weight is not None):
+            raise ValueError("out.u and out.pre_rstd go with pre_weight, out.post_rstd with post_weight")
+        if y is not None:
+            check_tensor("out.r", out.r, dev, (rows, d), dt)
+        if pre_weight is not None:
+            check_tensor("out.u", out.u, dev, (rows, d), dt)
+            check_tensor("out.pre_rstd", out.pre_rstd, dev, (rows,), torch.float32)
+        if post_weight is not None:
+            check_tensor("out.post_rstd", out.post_rstd, dev, (rows,), torch.float32)
+    with on_stream(dev, stream, (x, y, gate, post_weight, pre_weight, *(out or ()))) as s:
+        if out is None:
+            out = BlockNorm(
+                r=torch.empty_like(x) if y is not None else x,
+                u=torch.empty_like(x) if pre_weight is not None else None,
+                post_rstd=torch.empty(rows, dtype=torch.float32, device=dev) if post_weight is not None else None,
+                pre_rstd=torch.empty(rows, dtype=torch.float32, device=dev) if pre_weight is not None else None)
+        elif y is None:
+            out = out._replace(r=x)
+        check(lib().moe_block_norm(_ptr(x), _ptr(y), _ptr(gate), kind, _ptr(post_weight), _ptr(pre_weight),
+                                   rows, d, DTYPES[dt], float(beta), float(eps),
+                                   _ptr(out.r) if y is not None else None, _ptr(out.u),
+                                   _ptr(out.post_rstd), _ptr(out.pre_rstd), s))
+    return out
+
+
+def block_norm_backward(fwd: BlockNorm, y: torch.Tensor | None, *, dr: torch.Tensor | None = None,
+                        du: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                        post_weight: torch.Tensor | None = None, pre_weight: torch.Tensor | None = None,
+                        beta: float = 1.0, stream: torch.cuda.Stream | None = None) -> BlockNormGrads:
+    """Gradients of block_norm from dr and du, the gradients of its r and u: `fwd` is its
+    result (u is not read), y and the parameters are its arguments.  dr may be None (zero)
+    when pre_weight is given."""
+    dev, rows, d, dt = rows_of("fwd.r", fwd.r)
+    kind = _params(dev, rows, d, gate, post_weight, pre_weight)
+    for name, t in (("y", y), ("dr", dr), ("du", du)):
+        if t is not None:
+            check_tensor(name, t, dev, (rows, d), dt)
+    if (du is not None) != (pre_weight is not None):
+        raise ValueError("du goes with pre_weight")
+    if dr is None and pre_weight is None:
+        raise ValueError("dr is required without pre_weight")
+    if post_weight is not None:
+        check_tensor("fwd.post_rstd", fwd.post_rstd, dev, (rows,), torch.float32)
+    if pre_weight is not None:
+        check_tensor("fwd.pre_rstd", fwd.pre_rstd, dev, (rows,), torch.float32)
+    with on_stream(dev, stream, (fwd.r, y, dr, du, gate, post_weight, pre_weight, fwd.post_rstd,
+                                 fwd.pre_rstd)) as s:
+        g = BlockNormGrads(
+            dx=torch.empty_like(fwd.r), dy=torch.empty_like(fwd.r) if y is not None else None,
+            d_gate=torch.empty_like(gate) if gate is not None else None,
+            d_post_weight=torch.empty(d, dtype=torch.float32, device=dev) if post_weight is not None else None,
+            d_pre_weight=torch.empty(d, dtype=torch.float32, device=dev) if pre_weight is not None else None)
+        size = lib().moe_block_norm_workspace(rows, d)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        check(lib().moe_block_norm_backward(
+            _ptr(y), _ptr(fwd.r), _ptr(dr), _ptr(du), _ptr(gate), kind, _ptr(post_weight), _ptr(pre_weight),
+            _ptr(fwd.post_rstd) if post_weight is not None else None,
+            _ptr(fwd.pre_rstd) if pre_weight is not None else None, rows, d, DTYPES[dt], float(beta),
+            _ptr(g.dx), _ptr(g.dy), _ptr(g.d_gate), _ptr(g.d_post_weight), _ptr(g.d_pre_weight),
+            _ptr(ws), size, s))
+    return g

@@ -14,8 +14,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe.so")
-SOURCES = [os.path.join(CSRC, "moe_api.cu"), os.path.join(CSRC, "moe_ep.cu"),
-           os.path.join(CSRC, "moe_noalloc.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("moe_api.cu", "moe_ep.cu", "moe_noalloc.cu", "moe_grouped.cu",
+                                           "moe_block_norm.cu", "moe_grad_clip.cu")]
 GENCODE = "arch=compute_100a,code=sm_100a"
 
 
@@ -29,7 +29,7 @@ def nvcc_path() -> str:
 def nvcc_cmd(out: str = LIB, extra: list[str] | None = None) -> list[str]:
     return [nvcc_path(), "-gencode", GENCODE, "-O3", "-lineinfo", "-std=c++17",
             "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-O2", "-shared",
-            "-I", INCLUDE, "-I", CSRC, *(extra or []), "-o", out, *SOURCES]
+            "--threads", "0", "-I", INCLUDE, "-I", CSRC, *(extra or []), "-o", out, *SOURCES]
 
 
 def _stale() -> bool:

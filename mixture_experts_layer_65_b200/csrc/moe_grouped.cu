@@ -1,0 +1,92 @@
+// moe_grouped.cu -- moe_grouped_mm, moe_grouped_mm_dgrad and moe_grouped_mm_wgrad
+// (include/moe.h): checks, the choice of kernel, TMA descriptors and the launch.
+#include "op_common.cuh"
+#include "grouped_mm.cuh"
+
+using namespace moe;
+
+namespace {
+
+struct Shape {
+  int32_t G;
+  int64_t rows;
+  int32_t n, k, dtype;
+};
+
+moe_status check_shape(const Shape& s) {
+  if (s.dtype != MOE_BF16 && s.dtype != MOE_FP32)
+    return fail(MOE_ERR_INVALID_ARG, "dtype=%d is not MOE_FP32 or MOE_BF16", s.dtype);
+  if (s.G < 1 || s.G > kGroupedMaxGroups)
+    return fail(MOE_ERR_UNSUPPORTED, "n_groups=%d outside [1, %d]", s.G, kGroupedMaxGroups);
+  if (s.n < 1 || s.k < 1) return fail(MOE_ERR_INVALID_ARG, "n and k must be positive");
+  if (s.n > (1 << 20) || s.k > (1 << 20)) return fail(MOE_ERR_UNSUPPORTED, "n=%d or k=%d above 2^20", s.n, s.k);
+  if (s.rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows must not be negative");
+  if (s.rows >= (int64_t(1) << 30)) return fail(MOE_ERR_UNSUPPORTED, "rows=%lld above 2^30", (long long)s.rows);
+  // tiles of the smallest kind, all groups together, are counted in 32 bits
+  const int64_t nt = (s.n + 63) / 64, kt = (s.k + 63) / 64;
+  const int64_t mt = (s.rows + 63) / 64 + s.G;
+  if (mt * (nt > kt ? nt : kt) >= (int64_t(1) << 31) || nt * kt * s.G >= (int64_t(1) << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "more than 2^31 tiles");
+  return MOE_OK;
+}
+
+template <typename T, int OP>
+cudaError_t launch_simt(const GroupedSimtArgs& a, int64_t tiles, int n_sms, cudaStream_t st) {
+  const int64_t most = (int64_t)n_sms * 6;
+  return launch_pdl(grouped_simt_kernel<T, OP>, dim3((unsigned)(tiles < most ? tiles : most)), dim3(kGsThreads), 0,
+                    st, a);
+}
+
+template <int OP>
+moe_status product(const void* a, const void* b, const int32_t* counts, const Shape& s, int accumulate,
+                   void* out, moe_stream_t stream) {
+  MOE_TRY(check_shape(s));
+  constexpr bool W = OP == kGroupedWgrad;
+  const size_t es = s.dtype == MOE_BF16 ? 2 : 4;
+  const size_t a_cols = OP == kGroupedMM ? s.k : s.n;
+  const size_t a_bytes = (size_t)s.rows * a_cols * es;
+  const size_t b_bytes = (W ? (size_t)s.rows * s.k : (size_t)s.G * s.n * s.k) * es;
+  const size_t o_bytes = W ? (size_t)s.G * s.n * s.k * 4 : (size_t)s.rows * (OP == kGroupedMM ? s.n : s.k) * es;
+  if (!W && s.rows == 0) return MOE_OK;   // nothing to write
+  if (!counts || !out || (s.rows > 0 && !a) || ((!W || s.rows > 0) && !b))
+    return fail(MOE_ERR_INVALID_ARG, "an input/output pointer is NULL");
+  if (misaligned(a, es) || misaligned(b, es) || misaligned(out, W ? 4 : es) || misaligned(counts, 4))
+    return fail(MOE_ERR_INVALID_ARG, "a pointer is not aligned to its type");
+  if (overlaps(out, o_bytes, a, a_bytes) || overlaps(out, o_bytes, b, b_bytes) ||
+      overlaps(out, o_bytes, counts, (size_t)s.G * 4))
+    return fail(MOE_ERR_INVALID_ARG, "the output overlaps an input");
+  int n_sms = 0;
+  MOE_TRY(op_device(&n_sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int out_cols = OP == kGroupedMM ? s.n : s.k;
+  GroupedSimtArgs p{a, b, counts, out, s.G, (int)s.rows, s.n, s.k, accumulate};
+  const int64_t nt = (out_cols + kGsBN - 1) / kGsBN;
+  const int64_t tiles = W ? (int64_t)s.G * nt * ((s.n + kGsBM - 1) / kGsBM)
+                          : ((s.rows + kGsBM - 1) / kGsBM + (s.G < s.rows ? s.G : s.rows)) * nt;
+  MOE_CUDA((s.dtype == MOE_BF16 ? launch_simt<__nv_bfloat16, OP>(p, tiles, n_sms, st)
+                                : launch_simt<float, OP>(p, tiles, n_sms, st)));
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_grouped_mm(const void* x, const void* w, const int32_t* counts, int32_t n_groups, int64_t rows,
+                          int32_t n, int32_t k, int32_t dtype, void* y, moe_stream_t stream) {
+  return product<kGroupedMM>(x, w, counts, Shape{n_groups, rows, n, k, dtype}, 0, y, stream);
+}
+
+moe_status moe_grouped_mm_dgrad(const void* dy, const void* w, const int32_t* counts, int32_t n_groups,
+                                int64_t rows, int32_t n, int32_t k, int32_t dtype, void* dx,
+                                moe_stream_t stream) {
+  return product<kGroupedDgrad>(dy, w, counts, Shape{n_groups, rows, n, k, dtype}, 0, dx, stream);
+}
+
+moe_status moe_grouped_mm_wgrad(const void* dy, const void* x, const int32_t* counts, int32_t n_groups,
+                                int64_t rows, int32_t n, int32_t k, int32_t dtype, int32_t accumulate,
+                                float* dw, moe_stream_t stream) {
+  return product<kGroupedWgrad>(dy, x, counts, Shape{n_groups, rows, n, k, dtype}, accumulate, dw, stream);
+}
+
+}  // extern "C"
