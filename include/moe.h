@@ -308,6 +308,11 @@ moe_status moe_grouped_mm_wgrad(const void* dy, const void* x, const int32_t* co
                                 int32_t n_groups, int64_t rows, int32_t n, int32_t k, int32_t dtype,
                                 int32_t accumulate, float* dw, moe_stream_t stream);
 
+/* Synchronise `stream`, then read and clear the current device's error word of the grouped
+ * products: MOE_ERR_DEVICE_CHECK if a kernel of an earlier call (on any stream) recorded an
+ * error, e.g. a bounded wait that ran out, else MOE_OK. */
+moe_status moe_grouped_device_status(moe_stream_t stream);
+
 /* ---------------------------------------------------------------------------------
  * The norms before and after a block, fused with its gate, the residual scale and the
  * residual add.  (The pages leave the norms out of their equations; a block of a trained

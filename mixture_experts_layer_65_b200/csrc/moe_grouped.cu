@@ -2,6 +2,7 @@
 // (include/moe.h): checks, the choice of kernel, TMA descriptors and the launch.
 #include "op_common.cuh"
 #include "grouped_mm.cuh"
+#include "grouped_tc.cuh"
 
 using namespace moe;
 
@@ -37,6 +38,61 @@ cudaError_t launch_simt(const GroupedSimtArgs& a, int64_t tiles, int n_sms, cuda
                     st, a);
 }
 
+// Clusters of the paired kernel that can be resident at once on the current device (asked for
+// once per device; also sets the kernel's shared-memory limit).
+template <int OP>
+moe_status pair_clusters(int device, int n_sms, int* out) {
+  static std::atomic<int> kept[64];
+  if (device < 64 && (*out = kept[device].load(std::memory_order_acquire)) > 0) return MOE_OK;
+  MOE_CUDA(cudaFuncSetAttribute((const void*)grouped_pair_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)kGemmSmemBytes));
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.gridDim = dim3(2 * (n_sms / 2), 1, 1);
+  lc.blockDim = dim3(kGpThreads, 1, 1);
+  lc.dynamicSmemBytes = kGemmSmemBytes;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  int n = 0;
+  MOE_CUDA(cudaOccupancyMaxActiveClusters(&n, (const void*)grouped_pair_kernel<OP>, &lc));
+  if (n < 1) return fail(MOE_ERR_UNSUPPORTED, "no CTA pair of the grouped product fits on this device");
+  if (device < 64) kept[device].store(n, std::memory_order_release);
+  *out = n;
+  return MOE_OK;
+}
+
+// The products on the tensor cores: bf16, widths in whole 16-byte vectors, aligned buffers.
+template <int OP>
+moe_status launch_tc(const void* a, const void* b, const int32_t* counts, const Shape& s, int accumulate,
+                     void* out, int device, int n_sms, cudaStream_t st) {
+  CUtensorMap tmA, tmB;
+  bool ok;
+  if (OP == kGroupedMM)
+    ok = encode_2d(&tmA, a, s.k, s.rows, 128) && encode_3d(&tmB, b, s.k, s.n, s.G, 128);
+  else if (OP == kGroupedDgrad)
+    ok = encode_2d(&tmA, a, s.n, s.rows, 128) && encode_3d(&tmB, b, s.k, s.n, s.G, 64);
+  else
+    ok = encode_2d(&tmA, a, s.n, s.rows, 64) && encode_2d(&tmB, b, s.k, s.rows, 64);
+  if (!ok) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for a grouped product's operand");
+  int clusters = 0;
+  MOE_TRY(pair_clusters<OP>(device, n_sms, &clusters));
+  const int out_cols = OP == kGroupedMM ? s.n : s.k;
+  const int64_t nt = (out_cols + kGemmBN - 1) / kGemmBN;
+  const int64_t tiles = OP == kGroupedWgrad
+                            ? s.G * nt * ((s.n + kPairBM - 1) / kPairBM)
+                            : ((s.rows + kPairBM - 1) / kPairBM + (s.G < s.rows ? s.G : s.rows)) * nt;
+  const int out_es = OP == kGroupedWgrad ? 4 : 2;
+  GroupedPairArgs p{counts, s.G, (int)s.rows, s.n, s.k, out, accumulate,
+                    !misaligned(out, 32) && (out_cols * out_es) % 32 == 0};
+  MOE_CUDA(launch_pdl(grouped_pair_kernel<OP>, dim3(2 * (unsigned)(tiles < clusters ? tiles : clusters)),
+                      dim3(kGpThreads), kGemmSmemBytes, st, tmA, tmB, p));
+  return MOE_OK;
+}
+
 template <int OP>
 moe_status product(const void* a, const void* b, const int32_t* counts, const Shape& s, int accumulate,
                    void* out, moe_stream_t stream) {
@@ -55,9 +111,12 @@ moe_status product(const void* a, const void* b, const int32_t* counts, const Sh
   if (overlaps(out, o_bytes, a, a_bytes) || overlaps(out, o_bytes, b, b_bytes) ||
       overlaps(out, o_bytes, counts, (size_t)s.G * 4))
     return fail(MOE_ERR_INVALID_ARG, "the output overlaps an input");
-  int n_sms = 0;
-  MOE_TRY(op_device(&n_sms));
+  int n_sms = 0, device = 0;
+  MOE_TRY(op_device(&n_sms, &device));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (s.dtype == MOE_BF16 && s.n % 8 == 0 && s.k % 8 == 0 && s.rows > 0 && aligned16(a) && aligned16(b) &&
+      aligned16(out))
+    return launch_tc<OP>(a, b, counts, s, accumulate, out, device, n_sms, st);
   const int out_cols = OP == kGroupedMM ? s.n : s.k;
   GroupedSimtArgs p{a, b, counts, out, s.G, (int)s.rows, s.n, s.k, accumulate};
   const int64_t nt = (out_cols + kGsBN - 1) / kGsBN;
@@ -87,6 +146,18 @@ moe_status moe_grouped_mm_wgrad(const void* dy, const void* x, const int32_t* co
                                 int64_t rows, int32_t n, int32_t k, int32_t dtype, int32_t accumulate,
                                 float* dw, moe_stream_t stream) {
   return product<kGroupedWgrad>(dy, x, counts, Shape{n_groups, rows, n, k, dtype}, accumulate, dw, stream);
+}
+
+moe_status moe_grouped_device_status(moe_stream_t stream) {
+  int n_sms = 0;
+  MOE_TRY(op_device(&n_sms));
+  MOE_CUDA(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
+  int code = 0;
+  MOE_CUDA(cudaMemcpyFromSymbol(&code, g_grouped_err, sizeof(int)));
+  if (code == 0) return MOE_OK;
+  const int none = 0;
+  MOE_CUDA(cudaMemcpyToSymbol(g_grouped_err, &none, sizeof(int)));
+  return fail(MOE_ERR_DEVICE_CHECK, "a grouped product recorded device error 0x%x", code);
 }
 
 }  // extern "C"

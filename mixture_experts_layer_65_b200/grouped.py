@@ -88,3 +88,11 @@ def grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor,
         check(lib().moe_grouped_mm_wgrad(dy.data_ptr(), x.data_ptr(), counts.data_ptr(), g, rows, n, k,
                                          DTYPES[dt], int(bool(accumulate)), out.data_ptr(), s))
     return out
+
+
+def device_status(device=None, stream: torch.cuda.Stream | None = None) -> None:
+    """Synchronise `stream` (default: the current stream of `device`) and raise if a grouped
+    product on that device recorded a device-side error."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with on_stream(dev, stream) as s:
+        check(lib().moe_grouped_device_status(s))
