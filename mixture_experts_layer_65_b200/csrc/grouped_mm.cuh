@@ -23,16 +23,12 @@ struct GroupTable {
   int32_t tile0[kGroupedMaxGroups + 1];
 };
 
-// Fill the table from counts: row0 an exclusive prefix sum, tile0 the prefix of each group's
-// tiles -- nt tiles per `bm` rows, or (bm == 0) nt tiles whatever its rows.  A negative count
-// counts as 0 and rows past `rows` are cut off, so no index leaves the buffers.  Called by
-// `nthreads` threads (a multiple of 32, at most 1024) numbered tid; ends with a barrier of the
-// whole CTA.
-__device__ __forceinline__ void group_table(GroupTable& t, const int32_t* counts, int G, int rows, int bm,
-                                            int nt) {
-  __shared__ int64_t s_rows[32];
-  __shared__ int64_t s_tiles[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+// The groups' first rows from counts: row0[g], and row0[G] the end of the last.  A negative
+// count counts as 0 and rows past `rows` are cut off, so no index leaves the buffers.  Called by
+// the whole CTA (a multiple of 32 threads); ends with a barrier.
+__device__ __forceinline__ void group_rows(int32_t* row0, const int32_t* counts, int G, int rows) {
+  __shared__ int64_t warp_rows[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // each thread owns a run of consecutive groups
   const int per = (G + (int)blockDim.x - 1) / (int)blockDim.x;
   const int g0 = tid * per < G ? tid * per : G;
@@ -48,43 +44,47 @@ __device__ __forceinline__ void group_table(GroupTable& t, const int32_t* counts
     const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
-  if (lane == 31) s_rows[warp] = inc;
+  if (lane == 31) warp_rows[warp] = inc;
   __syncthreads();
-  int64_t row = inc - c;
-  for (int w = 0; w < warp; ++w) row += s_rows[w];
-  // tiles of the run, from the clipped row ranges
-  auto clip = [&](int64_t r) { return r < rows ? (int)r : rows; };
-  int64_t tiles = 0, r = row;
+  int64_t r = inc - c;
+  for (int w = 0; w < warp; ++w) r += warp_rows[w];
   for (int g = g0; g < g1; ++g) {
+    row0[g] = r < rows ? (int)r : rows;
     const int n = __ldg(counts + g);
-    const int64_t e = r + (n > 0 ? n : 0);
-    tiles += bm ? (int64_t)((clip(e) - clip(r) + bm - 1) / bm) * nt : nt;
-    r = e;
+    r += n > 0 ? n : 0;
+    if (g == G - 1) row0[G] = r < rows ? (int)r : rows;
   }
-  inc = tiles;
+  __syncthreads();
+}
+
+// The table: first rows, and the tile prefix -- nt tiles per `bm` rows of a group, or (bm == 0)
+// nt tiles whatever its rows.  As group_rows.
+__device__ __forceinline__ void group_table(GroupTable& t, const int32_t* counts, int G, int rows, int bm,
+                                            int nt) {
+  __shared__ int32_t warp_tiles[32];
+  group_rows(t.row0, counts, G, rows);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (G + (int)blockDim.x - 1) / (int)blockDim.x;
+  const int g0 = tid * per < G ? tid * per : G;
+  const int g1 = g0 + per < G ? g0 + per : G;
+  auto tiles_of = [&](int g) { return bm ? (t.row0[g + 1] - t.row0[g] + bm - 1) / bm * nt : nt; };
+  int c = 0;
+  for (int g = g0; g < g1; ++g) c += tiles_of(g);
+  int inc = c;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
-  if (lane == 31) s_tiles[warp] = inc;
+  if (lane == 31) warp_tiles[warp] = inc;
   __syncthreads();
-  int64_t tile = inc - tiles;
-  for (int w = 0; w < warp; ++w) tile += s_tiles[w];
-  r = row;
+  int tile = inc - c;
+  for (int w = 0; w < warp; ++w) tile += warp_tiles[w];
   for (int g = g0; g < g1; ++g) {
-    const int n = __ldg(counts + g);
-    const int64_t e = r + (n > 0 ? n : 0);
-    t.row0[g] = clip(r);
-    t.tile0[g] = (int32_t)tile;
-    tile += bm ? (int64_t)((clip(e) - clip(r) + bm - 1) / bm) * nt : nt;
-    r = e;
-    if (g == G - 1) {
-      t.row0[G] = clip(r);
-      t.tile0[G] = (int32_t)tile;
-    }
+    t.tile0[g] = tile;
+    tile += tiles_of(g);
+    if (g == G - 1) t.tile0[G] = tile;
   }
-  (void)nw;
   __syncthreads();
 }
 

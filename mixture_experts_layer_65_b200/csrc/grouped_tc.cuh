@@ -1,4 +1,4 @@
-// grouped_tc.cuh -- the products of grouped_mm.cuh on the tensor cores (bf16 operands).
+// grouped_tc.cuh -- mm and dgrad of grouped_mm.cuh on the tensor cores (bf16 operands).
 //
 // grouped_pair_kernel: persistent clusters of two CTAs, 256 x 256 output tiles, tcgen05.mma
 // with cta_group::2 (M = 256), the roles and the ring of gemm_tc.cuh.  The operands are read
@@ -7,14 +7,8 @@
 // wgrad) as an MN-major tile -- boxes of 64 output columns x 64 contraction rows, 128-byte
 // swizzled, which the MMA reads through the descriptor's strides.
 //
-// Ragged rows:
-//   mm, dgrad  an expert's last row tile reads on into the next expert's rows; those
-//              accumulator rows are computed and not stored.
-//   wgrad      the rows are the contraction: the last k-block runs only ceil(t / 16) of its
-//              four MMA steps for t rows, and the rows behind t in the last step are zeroed in
-//              both operands (0 x NaN would be NaN) by a warp of each CTA before the MMA:
-//              that k-block's loads complete on a barrier of the CTA, and the zeroing warp
-//              arrives on the leader's "full" barrier in its stead.
+// An expert's last row tile reads on into the next expert's rows; those accumulator rows are
+// computed and not stored.
 #pragma once
 
 #include "gemm_tc.cuh"
@@ -26,7 +20,7 @@ namespace moe {
 static __device__ int g_grouped_err;
 
 constexpr int kGpEpiWarps = 8;
-constexpr int kGpThreads = 64 + 32 * (kGpEpiWarps + 1);   // + the zeroing warp
+constexpr int kGpThreads = 64 + 32 * kGpEpiWarps;
 constexpr uint32_t kGpBox = 64 * 128;                     // one MN-major box: 64 rows of 128 bytes
 
 struct GroupedPairArgs {
@@ -97,8 +91,7 @@ __device__ __forceinline__ GpTile gp_tile(const GroupTable& t, const GroupedPair
   c.n = local - c.m * nt;
   c.row0 = t.row0[g];
   c.grows = t.row0[g + 1] - c.row0;
-  const int q = OP == kGroupedMM ? a.K : OP == kGroupedDgrad ? a.N : c.grows;
-  c.kb = (q + kGemmBK - 1) / kGemmBK;
+  c.kb = ((OP == kGroupedMM ? a.K : a.N) + kGemmBK - 1) / kGemmBK;
   return c;
 }
 
@@ -106,8 +99,7 @@ template <int OP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
 grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     GroupedPairArgs a) {
-  constexpr bool W = OP == kGroupedWgrad;
-  constexpr bool kAMn = W, kBMn = OP != kGroupedMM;
+  constexpr bool kBMn = OP == kGroupedDgrad;
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   __shared__ GroupTable tab;
@@ -119,8 +111,7 @@ grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
   uint64_t* acc_full = empty + kGemmStages;             // both CTAs
   uint64_t* acc_empty = acc_full + 2;                   // used in the leader
   uint64_t* drain = acc_empty + 2;                      // both CTAs
-  uint64_t* tail = drain + 1;                           // both CTAs (wgrad): loads of a tail stage
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + kGemmStages);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* err = &g_grouped_err;
 
@@ -131,10 +122,8 @@ grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kGemmStages; ++s) {
-      // wgrad: one arrival per CTA (its producer, or its zeroing warp for a tail stage)
-      mbar_init(smem_u32(&full[s]), W ? 2 : 1);
+      mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
-      mbar_init(smem_u32(&tail[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&acc_full[s]), 1);
@@ -157,7 +146,7 @@ grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
   pdl_wait();
   const int out_cols = OP == kGroupedMM ? a.N : a.K;
   const int nt = (out_cols + kGemmBN - 1) / kGemmBN;
-  group_table(tab, a.counts, a.G, a.rows, W ? 0 : kPairBM, W ? nt * ((a.N + kPairBM - 1) / kPairBM) : nt);
+  group_table(tab, a.counts, a.G, a.rows, kPairBM, nt);
   const int total = tab.tile0[a.G];
 
   // columns of a tile, as the MMA's N: a multiple of 32 (each CTA holds half of B's rows)
@@ -165,9 +154,6 @@ grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     const int left = out_cols - n * kGemmBN;
     return left >= kGemmBN ? kGemmBN : (left + 31) & ~31;
   };
-  // rows of a wgrad tile's last k-block that the MMA reads and that are not the expert's:
-  // [t, 16 ceil(t / 16)), none when t is a multiple of 16
-  auto tail_rows = [&](const GpTile& c) { return c.grows - (c.kb - 1) * kGemmBK; };
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
@@ -178,35 +164,25 @@ grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
       for (int tile = cid; tile < total && ok; tile += ncl) {
         const GpTile c = gp_tile<OP>(tab, a, nt, tile, g);
         // this CTA's 128 rows of A (output rows) and half of B's rows (output columns)
-        const int a0 = (W ? 0 : c.row0) + c.m * kPairBM + (int)rank * 128;
+        const int a0 = c.row0 + c.m * kPairBM + (int)rank * 128;
         const int b0 = c.n * kGemmBN + (int)rank * (tile_cols(c.n) / 2);
         for (int kb0 = 0; kb0 < c.kb; kb0 += kGemmKPS) {
           ok = mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, err, kErrWaitProducer);
           if (!ok) break;
           const uint32_t sa = smem_u32(base + (size_t)stage * kGemmStageBytes);
           const int nk = c.kb - kb0 < kGemmKPS ? c.kb - kb0 : kGemmKPS;
-          const uint32_t bytes = (uint32_t)nk * (kGemmABytes + kGemmBBytes);   // this CTA's
-          const bool fix = W && kb0 + nk == c.kb && (tail_rows(c) & 15) != 0;
-          const uint32_t fb = fix ? mapa_shared(smem_u32(&tail[stage]), rank) : mapa_shared(smem_u32(&full[stage]), 0);
-          if (fix) mbar_arrive_expect_tx(smem_u32(&tail[stage]), bytes);
-          else if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2u * bytes);
-          else if (W) mbar_arrive_cluster(fb);
+          const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+          if (leader)
+            mbar_arrive_expect_tx(smem_u32(&full[stage]), 2u * (uint32_t)nk * (kGemmABytes + kGemmBBytes));
           for (int j = 0; j < nk; ++j) {
             const int q = (kb0 + j) * kGemmBK;   // contraction index
             const uint32_t da = sa + j * kGemmABytes, db = sa + kGemmBOff + j * kGemmBBytes;
-            if constexpr (W) {
-              tma_load_2d_pair(da, &tmA, fb, a0, c.row0 + q);
-              tma_load_2d_pair(da + kGpBox, &tmA, fb, a0 + 64, c.row0 + q);
-              tma_load_2d_pair(db, &tmB, fb, b0, c.row0 + q);
-              tma_load_2d_pair(db + kGpBox, &tmB, fb, b0 + 64, c.row0 + q);
+            tma_load_2d_pair(da, &tmA, fb, q, a0);
+            if constexpr (!kBMn) {
+              tma_load_3d_pair(db, &tmB, fb, q, b0, c.g);
             } else {
-              tma_load_2d_pair(da, &tmA, fb, q, a0);
-              if constexpr (OP == kGroupedMM) {
-                tma_load_3d_pair(db, &tmB, fb, q, b0, c.g);
-              } else {
-                tma_load_3d_pair(db, &tmB, fb, b0, q, c.g);
-                tma_load_3d_pair(db + kGpBox, &tmB, fb, b0 + 64, q, c.g);
-              }
+              tma_load_3d_pair(db, &tmB, fb, b0, q, c.g);
+              tma_load_3d_pair(db + kGpBox, &tmB, fb, b0 + 64, q, c.g);
             }
           }
           if (++stage == kGemmStages) { stage = 0; phase ^= 1u; }
@@ -228,38 +204,30 @@ grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
       int stage = 0, g = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tile = cid; tile < total && ok; tile += ncl) {
+      for (int tile = cid; tile < total && ok; tile += ncl, ++it) {
         const GpTile c = gp_tile<OP>(tab, a, nt, tile, g);
-        if (W && c.kb == 0) continue;   // no rows: the epilogue writes zeros by itself
-        const uint32_t idesc =
-            idesc_bf16_f32(kPairBM, tile_cols(c.n)) | (kAMn ? kIdescAMn : 0u) | (kBMn ? kIdescBMn : 0u);
+        const uint32_t idesc = idesc_bf16_f32(kPairBM, tile_cols(c.n)) | (kBMn ? kIdescBMn : 0u);
         const int acc = it & 1;
         const uint32_t acc_par = (it >> 1) & 1;
-        ++it;
         ok = mbar_wait(smem_u32(&acc_empty[acc]), acc_par ^ 1u, abort_flag, err, kErrWaitMma);
         if (!ok) break;
         tc_fence_after();
         const uint32_t dt = tmem_base + static_cast<uint32_t>(acc * kGemmBN);
         for (int kb0 = 0; kb0 < c.kb; kb0 += kGemmKPS) {
-          ok = W ? mbar_wait_cluster(smem_u32(&full[stage]), phase, abort_flag, err, kErrWaitMma)
-                 : mbar_wait(smem_u32(&full[stage]), phase, abort_flag, err, kErrWaitMma);
+          ok = mbar_wait(smem_u32(&full[stage]), phase, abort_flag, err, kErrWaitMma);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sa = smem_u32(base + (size_t)stage * kGemmStageBytes);
           const int nk = c.kb - kb0 < kGemmKPS ? c.kb - kb0 : kGemmKPS;
           for (int j = 0; j < nk; ++j) {
             const uint32_t pa = sa + j * kGemmABytes, pb = sa + kGemmBOff + j * kGemmBBytes;
-            const uint64_t ad = kAMn ? sdesc_mn_sw128(pa) : sdesc_k_sw128(pa);
+            const uint64_t ad = sdesc_k_sw128(pa);
             const uint64_t bd = kBMn ? sdesc_mn_sw128(pb) : sdesc_k_sw128(pb);
             // 16 contraction values a step: 32 bytes along a K-major row, 16 rows of 128 bytes
             // of an MN-major box
-            int steps = 4;
-            if (W && kb0 + j == c.kb - 1) steps = (tail_rows(c) + 15) >> 4;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (k < steps)
-                tc_mma_f16_pair(dt, ad + (kAMn ? 128u : 2u) * k, bd + (kBMn ? 128u : 2u) * k, idesc,
-                                (kb0 | j | k) != 0);
+              tc_mma_f16_pair(dt, ad + 2u * k, bd + (kBMn ? 128u : 2u) * k, idesc, (kb0 | j | k) != 0);
           }
           tc_commit_pair_mc(smem_u32(&empty[stage]), 0x3);
           if (++stage == kGemmStages) { stage = 0; phase ^= 1u; }
@@ -269,124 +237,52 @@ grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
       tc_commit_pair_mc(smem_u32(drain), 0x3);
     }
     __syncwarp();
-  } else if (warp == 2 + kGpEpiWarps) {
-    // ------------------------------------------------------------------ zeroing of tail rows
-    if constexpr (W) {
-      int stage = 0, g = 0;
-      uint32_t tail_phase = 0;   // a bit per stage
-      for (int tile = cid; tile < total; tile += ncl) {
-        const GpTile c = gp_tile<OP>(tab, a, nt, tile, g);
-        if (c.kb == 0) continue;
-        const int stages = (c.kb + kGemmKPS - 1) / kGemmKPS;
-        const int last = (stage + stages - 1) % kGemmStages;
-        stage = (stage + stages) % kGemmStages;
-        const int t = tail_rows(c);
-        if ((t & 15) == 0) continue;
-        int ok = 1;
-        if (lane == 0) ok = mbar_wait(smem_u32(&tail[last]), tail_phase >> last & 1u, abort_flag, err, kErrWaitDrain);
-        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-        __syncwarp();
-        tail_phase ^= 1u << last;
-        // rows [t, 16 ceil(t / 16)) of the stage's last k-block: two boxes each of A and B, 128
-        // bytes a row (the swizzle permutes 16-byte chunks within a row)
-        uint8_t* sp = base + (size_t)last * kGemmStageBytes;
-        const int j = (c.kb - 1) % kGemmKPS;
-        const int nz = ((t + 15) & ~15) - t;
-        for (int i = lane; i < nz * 32; i += 32) {
-          const int row = t + (i >> 5), box = (i >> 3) & 3, chunk = i & 7;
-          uint8_t* p = sp + (box < 2 ? j * kGemmABytes : kGemmBOff + j * kGemmBBytes) + (box & 1) * kGpBox +
-                       row * 128 + chunk * 16;
-          *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_shared();   // the zeros, before the tensor cores read the stage
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[last]), 0));
-      }
-    }
   } else {
     // ------------------------------------------------------------------ epilogue
     const int q = warp & 3;                 // TMEM lane quadrant
     const int half = (warp - 2) >> 2;       // which half of the tile's columns
     const int rr = q * 32 + lane;
     int g = 0, it = 0;
-    for (int tile = cid; tile < total; tile += ncl) {
+    for (int tile = cid; tile < total; tile += ncl, ++it) {
       const GpTile c = gp_tile<OP>(tab, a, nt, tile, g);
-      const bool zero = W && c.kb == 0;
-      if (zero && a.accumulate) continue;
       const int acc = it & 1;
       const uint32_t acc_par = (it >> 1) & 1;
-      if (!zero) {
-        ++it;
-        int ok = 1;
-        if (lane == 0) ok = mbar_wait(smem_u32(&acc_full[acc]), acc_par, abort_flag, err, kErrWaitEpilogue);
-        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-        tc_fence_after();
-      }
+      int ok = 1;
+      if (lane == 0) ok = mbar_wait(smem_u32(&acc_full[acc]), acc_par, abort_flag, err, kErrWaitEpilogue);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      tc_fence_after();
       const uint32_t trow =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kGemmBN);
-      const int mrow = c.m * kPairBM + (int)rank * 128 + rr;   // row of the expert / of dW
-      const bool row_ok = mrow < (W ? a.N : c.grows);
-      const size_t orow = W ? (size_t)c.g * a.N + mrow : (size_t)c.row0 + mrow;
+      const int mrow = c.m * kPairBM + (int)rank * 128 + rr;   // row of the expert
+      const bool row_ok = mrow < c.grows;
+      const size_t orow = (size_t)c.row0 + mrow;
 #pragma unroll 1
       for (int cc = half * (kGemmBN / 2); cc < (half + 1) * (kGemmBN / 2); cc += 32) {
         const int col = c.n * kGemmBN + cc;
         if (col >= out_cols) break;
         uint32_t v[32];
         __syncwarp();
-        if (zero) {
-#pragma unroll
-          for (int x = 0; x < 32; ++x) v[x] = 0u;
-        } else {
-          tmem_ld32(trow + static_cast<uint32_t>(cc), v);
-          tmem_ld_wait(v);
-        }
+        tmem_ld32(trow + static_cast<uint32_t>(cc), v);
+        tmem_ld_wait(v);
         if (!row_ok) continue;
         const int left = out_cols - col;   // a multiple of 8
-        if constexpr (W) {
-          float* o = static_cast<float*>(a.out) + orow * out_cols + col;
-          if (a.accumulate) {
+        uint32_t pk[16];
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              if (4 * x < left) {
-                const float4 p = *reinterpret_cast<const float4*>(o + 4 * x);
-                v[4 * x] = __float_as_uint(p.x + __uint_as_float(v[4 * x]));
-                v[4 * x + 1] = __float_as_uint(p.y + __uint_as_float(v[4 * x + 1]));
-                v[4 * x + 2] = __float_as_uint(p.z + __uint_as_float(v[4 * x + 2]));
-                v[4 * x + 3] = __float_as_uint(p.w + __uint_as_float(v[4 * x + 3]));
-              }
-          }
+        for (int i = 0; i < 16; ++i)
+          pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + orow * out_cols + col;
+        if (a.wide && left >= 32) {
+          st_global_v8(o, make_uint4(pk[0], pk[1], pk[2], pk[3]), make_uint4(pk[4], pk[5], pk[6], pk[7]));
+          st_global_v8(o + 16, make_uint4(pk[8], pk[9], pk[10], pk[11]),
+                       make_uint4(pk[12], pk[13], pk[14], pk[15]));
+        } else {
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            if (8 * x < left) {
-              const uint4 lo = make_uint4(v[8 * x], v[8 * x + 1], v[8 * x + 2], v[8 * x + 3]);
-              const uint4 hi = make_uint4(v[8 * x + 4], v[8 * x + 5], v[8 * x + 6], v[8 * x + 7]);
-              if (a.wide) {
-                st_global_v8(o + 8 * x, lo, hi);
-              } else {
-                *reinterpret_cast<uint4*>(o + 8 * x) = lo;
-                *reinterpret_cast<uint4*>(o + 8 * x + 4) = hi;
-              }
-            }
-        } else {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + orow * out_cols + col;
-          if (a.wide && left >= 32) {
-            st_global_v8(o, make_uint4(pk[0], pk[1], pk[2], pk[3]), make_uint4(pk[4], pk[5], pk[6], pk[7]));
-            st_global_v8(o + 16, make_uint4(pk[8], pk[9], pk[10], pk[11]),
-                         make_uint4(pk[12], pk[13], pk[14], pk[15]));
-          } else {
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (8 * x < left)
-                *reinterpret_cast<uint4*>(o + 8 * x) =
-                    make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
-          }
+            if (8 * x < left)
+              *reinterpret_cast<uint4*>(o + 8 * x) =
+                  make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
         }
       }
-      if (zero) continue;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[acc]), 0));

@@ -1,0 +1,392 @@
+// grouped_wgrad.cuh -- the weight gradients of grouped_mm.cuh on the tensor cores (bf16 operands,
+// fp32 result): dW_e = dy_e^T x_e, a product whose contraction runs over the expert's rows.
+//
+// Clusters of two CTAs, 256 x 256 tiles of dW_e, tcgen05.mma with cta_group::2.  dy and x are read
+// where they lie: their contiguous index is an output index, so both operands are MN-major
+// tiles (boxes of 64 columns x 64 rows).
+//
+// Precision: the tensor cores truncate when they add to an accumulator, which over n steps of
+// 16 rows leaves a bias of about 2.2e-8 n of the value (measured: 7.4e-6 of dW's norm when an
+// expert had 10,800 rows in one chain).  So a chain is cut after kGwChunk k-blocks of 64
+// rows: the epilogue warps add the pieces in registers with round-to-nearest while the MMA
+// fills the other accumulator.
+//
+// Ragged rows: a tile's last k-block runs ceil(t / 16) of its four MMA steps for t rows, and
+// the rows behind t in the last step are zeroed in both operands (0 x NaN would be NaN) by a
+// warp of each CTA before the MMA: that stage's loads complete on a barrier of the CTA, and
+// the zeroing warp arrives on the leader's "full" barrier in its stead.
+//
+// Balance: a tile's time goes with its expert's rows, which may differ a hundredfold.  The
+// grid has one cluster per tile, experts with most rows first; a running cluster takes the
+// next unstarted one over (clusterlaunchcontrol), so no cluster is left with a long tile at
+// the end, and which cluster computes a tile does not change its value.
+#pragma once
+
+#include "grouped_tc.cuh"
+
+namespace moe {
+
+constexpr int kGwChunk = 8;                                // k-blocks per accumulator chain
+constexpr int kGwThreads = 64 + 32 * (kGpEpiWarps + 1);    // + the zeroing warp
+constexpr int kGwSlots = 4;                                // tiles taken over ahead
+// arrivals that free a slot: in each CTA the producer, the zeroing warp and the epilogue
+// warps, in the leader also the MMA issuer
+constexpr int kGwReaders = 2 * (2 + kGpEpiWarps) + 1;
+static_assert(kGwChunk % kGemmKPS == 0, "a stage belongs to one chain");
+
+// The experts' first rows, and the experts in order of falling row counts.
+struct WgradTable {
+  int32_t row0[kGroupedMaxGroups + 1];
+  int32_t order[kGroupedMaxGroups];
+};
+
+// Take over the next cluster of the grid that has not started: its answer (16 bytes) arrives
+// at the same offset of both CTAs' shared memory, counted on the barrier at the same offset.
+__device__ __forceinline__ void clc_try_cancel(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+      ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(answer),
+      "r"(bar)
+      : "memory");
+}
+// The first CTA of the cluster taken over, or -1 when none was left.
+__device__ __forceinline__ int clc_answer(uint32_t answer) {
+  uint32_t x, ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}\n"
+      : "=r"(x), "=r"(ok)
+      : "r"(answer)
+      : "memory");
+  return ok ? static_cast<int>(x) : -1;
+}
+
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
+               "r"(bytes)
+               : "memory");
+}
+
+static __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGwThreads, 1)
+grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     GroupedPairArgs a) {
+  pdl_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ WgradTable tab;
+  __shared__ __align__(16) uint8_t answers[kGwSlots][16];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* ctl = base + (size_t)kGemmStages * kGemmStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ctl);   // used in the leader
+  uint64_t* empty = full + kGemmStages;                 // both CTAs
+  uint64_t* acc_full = empty + kGemmStages;             // both CTAs
+  uint64_t* acc_empty = acc_full + 2;                   // used in the leader
+  uint64_t* drain = acc_empty + 2;                      // both CTAs
+  uint64_t* tail = drain + 1;                           // both CTAs: loads of a tail stage
+  uint64_t* next_full = tail + kGemmStages;             // both CTAs: an answer has arrived
+  uint64_t* next_empty = next_full + kGwSlots;          // used in the leader: all have read it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(next_empty + kGwSlots);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* err = &g_grouped_err;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kGemmStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 2);    // each CTA's producer, or its zeroing warp
+      mbar_init(smem_u32(&empty[s]), 1);
+      mbar_init(smem_u32(&tail[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&acc_full[s]), 1);
+      mbar_init(smem_u32(&acc_empty[s]), 2 * kGpEpiWarps);
+    }
+    for (int s = 0; s < kGwSlots; ++s) {
+      mbar_init(smem_u32(&next_full[s]), 1);
+      mbar_init(smem_u32(&next_empty[s]), kGwReaders);
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), kGemmTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  const int nt = (a.K + kGemmBN - 1) / kGemmBN;                    // column tiles of a gradient
+  const int per_group = nt * ((a.N + kPairBM - 1) / kPairBM);
+  group_rows(tab.row0, a.counts, a.G, a.rows);
+  for (int g = threadIdx.x; g < a.G; g += kGwThreads) {
+    const int n = tab.row0[g + 1] - tab.row0[g];
+    int before = 0;
+    for (int h = 0; h < a.G; ++h) {
+      const int m = tab.row0[h + 1] - tab.row0[h];
+      before += m > n || (m == n && h < g);
+    }
+    tab.order[before] = g;
+  }
+  __syncthreads();
+
+  auto tile_of = [&](int tile) {
+    GpTile c;
+    const int o = tile / per_group, local = tile - o * per_group;
+    c.g = tab.order[o];
+    c.m = local / nt;
+    c.n = local - c.m * nt;
+    c.row0 = tab.row0[c.g];
+    c.grows = tab.row0[c.g + 1] - c.row0;
+    c.kb = (c.grows + kGemmBK - 1) / kGemmBK;
+    return c;
+  };
+  auto tile_cols = [&](int n) {   // the MMA's N: a multiple of 32
+    const int left = a.K - n * kGemmBN;
+    return left >= kGemmBN ? kGemmBN : (left + 31) & ~31;
+  };
+  auto tail_rows = [&](const GpTile& c) { return c.grows - (c.kb - 1) * kGemmBK; };
+  // The next tile (one thread of each reader), or -1: none left, or a wait ran out.
+  struct Next {
+    int slot = 0;
+    uint32_t phase = 0;
+  };
+  auto next_tile = [&](Next& nx) {
+    if (!mbar_wait_cluster(smem_u32(&next_full[nx.slot]), nx.phase, abort_flag, err, kErrWaitProducer)) return -1;
+    const int cta = clc_answer(smem_u32(answers[nx.slot]));
+    fence_proxy_async_shared();   // read before the next answer is written
+    mbar_arrive_cluster(mapa_shared(smem_u32(&next_empty[nx.slot]), 0));
+    if (++nx.slot == kGwSlots) { nx.slot = 0; nx.phase ^= 1u; }
+    return cta < 0 ? -1 : cta >> 1;
+  };
+
+  const int first = blockIdx.x >> 1;
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      Next nx;
+      for (int tile = first; tile >= 0 && ok;) {
+        if (leader) {   // ask for the tile after this one
+          ok = mbar_wait_cluster(smem_u32(&next_empty[nx.slot]), nx.phase ^ 1u, abort_flag, err, kErrWaitProducer);
+          if (!ok) break;
+          mbar_arrive_expect_tx(smem_u32(&next_full[nx.slot]), 16);
+          mbar_arrive_expect_tx_cluster(mapa_shared(smem_u32(&next_full[nx.slot]), 1), 16);
+          clc_try_cancel(smem_u32(answers[nx.slot]), smem_u32(&next_full[nx.slot]));
+        }
+        const GpTile c = tile_of(tile);
+        const int a0 = c.m * kPairBM + (int)rank * 128;
+        const int b0 = c.n * kGemmBN + (int)rank * (tile_cols(c.n) / 2);
+        for (int kb0 = 0; kb0 < c.kb; kb0 += kGemmKPS) {
+          ok = mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, err, kErrWaitProducer);
+          if (!ok) break;
+          const uint32_t sa = smem_u32(base + (size_t)stage * kGemmStageBytes);
+          const int nk = c.kb - kb0 < kGemmKPS ? c.kb - kb0 : kGemmKPS;
+          const uint32_t bytes = (uint32_t)nk * (kGemmABytes + kGemmBBytes);   // this CTA's
+          const bool fix = kb0 + nk == c.kb && (tail_rows(c) & 15) != 0;
+          const uint32_t fb =
+              fix ? mapa_shared(smem_u32(&tail[stage]), rank) : mapa_shared(smem_u32(&full[stage]), 0);
+          if (fix) mbar_arrive_expect_tx(smem_u32(&tail[stage]), bytes);
+          else if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2u * bytes);
+          else mbar_arrive_cluster(fb);
+          for (int j = 0; j < nk; ++j) {
+            const int row = c.row0 + (kb0 + j) * kGemmBK;
+            const uint32_t da = sa + j * kGemmABytes, db = sa + kGemmBOff + j * kGemmBBytes;
+            tma_load_2d_pair(da, &tmA, fb, a0, row);
+            tma_load_2d_pair(da + kGpBox, &tmA, fb, a0 + 64, row);
+            tma_load_2d_pair(db, &tmB, fb, b0, row);
+            tma_load_2d_pair(db + kGpBox, &tmB, fb, b0 + 64, row);
+          }
+          if (++stage == kGemmStages) { stage = 0; phase ^= 1u; }
+        }
+        if (ok) tile = next_tile(nx);
+      }
+      if (!ok) {   // gave up: let the copies in flight land before the CTA's memory is handed on
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+      } else {   // every stage released: no copy of this CTA is in flight
+        for (int s = 0; s < kGemmStages; ++s) {
+          if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, err, kErrWaitDrain)) break;
+          if (++stage == kGemmStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0 && leader) {
+      int stage = 0, it = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      Next nx;
+      for (int tile = first; tile >= 0 && ok;) {
+        const GpTile c = tile_of(tile);
+        const uint32_t idesc = idesc_bf16_f32(kPairBM, tile_cols(c.n)) | kIdescAMn | kIdescBMn;
+        for (int kc = 0; kc < c.kb && ok; kc += kGwChunk, ++it) {
+          const int kend = c.kb - kc < kGwChunk ? c.kb : kc + kGwChunk;
+          const int acc = it & 1;
+          ok = mbar_wait(smem_u32(&acc_empty[acc]), ((it >> 1) & 1) ^ 1u, abort_flag, err, kErrWaitMma);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t dt = tmem_base + static_cast<uint32_t>(acc * kGemmBN);
+          for (int kb0 = kc; kb0 < kend; kb0 += kGemmKPS) {
+            ok = mbar_wait_cluster(smem_u32(&full[stage]), phase, abort_flag, err, kErrWaitMma);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sa = smem_u32(base + (size_t)stage * kGemmStageBytes);
+            const int nk = kend - kb0 < kGemmKPS ? kend - kb0 : kGemmKPS;
+            for (int j = 0; j < nk; ++j) {
+              const uint64_t ad = sdesc_mn_sw128(sa + j * kGemmABytes);
+              const uint64_t bd = sdesc_mn_sw128(sa + kGemmBOff + j * kGemmBBytes);
+              // 16 rows of 128 bytes a step
+              const int steps = kb0 + j == c.kb - 1 ? (tail_rows(c) + 15) >> 4 : 4;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (k < steps) tc_mma_f16_pair(dt, ad + 128u * k, bd + 128u * k, idesc, (kb0 != kc) | j | k);
+            }
+            tc_commit_pair_mc(smem_u32(&empty[stage]), 0x3);
+            if (++stage == kGemmStages) { stage = 0; phase ^= 1u; }
+          }
+          if (ok) tc_commit_pair_mc(smem_u32(&acc_full[acc]), 0x3);
+        }
+        if (ok) tile = next_tile(nx);
+      }
+      tc_commit_pair_mc(smem_u32(drain), 0x3);
+    }
+    __syncwarp();
+  } else if (warp == 2 + kGpEpiWarps) {
+    // ------------------------------------------------------------------ zeroing of tail rows
+    int stage = 0;
+    uint32_t tail_phase = 0;   // a bit per stage
+    Next nx;
+    for (int tile = first; tile >= 0;) {
+      const GpTile c = tile_of(tile);
+      const int stages = (c.kb + kGemmKPS - 1) / kGemmKPS;
+      const int last = (stage + stages + kGemmStages - 1) % kGemmStages;
+      stage = (stage + stages) % kGemmStages;
+      const int t = tail_rows(c);
+      if (c.kb > 0 && (t & 15) != 0) {
+        int ok = 1;
+        if (lane == 0) ok = mbar_wait(smem_u32(&tail[last]), tail_phase >> last & 1u, abort_flag, err, kErrWaitDrain);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        __syncwarp();
+        tail_phase ^= 1u << last;
+        // rows [t, 16 ceil(t / 16)) of the stage's last k-block: two boxes each of A and B, 128
+        // bytes a row (the swizzle permutes 16-byte chunks within a row)
+        uint8_t* sp = base + (size_t)last * kGemmStageBytes;
+        const int j = (c.kb - 1) % kGemmKPS;
+        const int nz = ((t + 15) & ~15) - t;
+        for (int i = lane; i < nz * 32; i += 32) {
+          const int row = t + (i >> 5), box = (i >> 3) & 3, chunk = i & 7;
+          uint8_t* p = sp + (box < 2 ? j * kGemmABytes : kGemmBOff + j * kGemmBBytes) + (box & 1) * kGpBox +
+                       row * 128 + chunk * 16;
+          *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_shared();   // the zeros, before the tensor cores read the stage
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[last]), 0));
+      }
+      if (lane == 0) tile = next_tile(nx);
+      tile = __shfl_sync(0xffffffffu, tile, 0);
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    const int q = warp & 3;                 // TMEM lane quadrant
+    const int half = (warp - 2) >> 2;       // which half of the tile's columns
+    const int rr = q * 32 + lane;
+    int it = 0;
+    Next nx;
+    for (int tile = first; tile >= 0;) {
+      const GpTile c = tile_of(tile);
+      // this thread's row of 128 columns; an expert without rows leaves zeros
+      uint32_t s[4][32];
+      if (c.kb == 0) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[x][i] = 0u;
+      }
+      int ok = 1;
+      for (int kc = 0; kc < c.kb; kc += kGwChunk, ++it) {
+        const int acc = it & 1;
+        if (lane == 0) ok = mbar_wait(smem_u32(&acc_full[acc]), (it >> 1) & 1, abort_flag, err, kErrWaitEpilogue);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t trow = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                              static_cast<uint32_t>(acc * kGemmBN + half * (kGemmBN / 2));
+        if (kc == 0) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) tmem_ld32(trow + 32u * x, s[x]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) tmem_ld_wait(s[x]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t v[32];
+            tmem_ld32(trow + 32u * x, v);
+            tmem_ld_wait(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              s[x][i] = __float_as_uint(__fadd_rn(__uint_as_float(s[x][i]), __uint_as_float(v[i])));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[acc]), 0));
+      }
+      if (!ok) break;
+      const int mrow = c.m * kPairBM + (int)rank * 128 + rr;
+      if (mrow < a.N && !(c.kb == 0 && a.accumulate)) {
+        const int col0 = c.n * kGemmBN + half * (kGemmBN / 2);
+        float* o = static_cast<float*>(a.out) + ((size_t)c.g * a.N + mrow) * a.K + col0;
+        const int left = a.K - col0;   // a multiple of 8
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          if (8 * x >= left) break;
+          uint32_t* v = &s[x >> 2][(x & 3) * 8];
+          if (a.accumulate) {
+            const float4 p0 = *reinterpret_cast<const float4*>(o + 8 * x);
+            const float4 p1 = *reinterpret_cast<const float4*>(o + 8 * x + 4);
+            const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(p[i] + __uint_as_float(v[i]));
+          }
+          const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
+          if (a.wide) {
+            st_global_v8(o + 8 * x, lo, hi);
+          } else {
+            *reinterpret_cast<uint4*>(o + 8 * x) = lo;
+            *reinterpret_cast<uint4*>(o + 8 * x + 4) = hi;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tile = next_tile(nx);
+      tile = __shfl_sync(0xffffffffu, tile, 0);
+    }
+  }
+
+  // teardown: all MMAs of the pair have completed before TMEM is released in either CTA
+  if (warp == 1 && lane == 0) mbar_wait(smem_u32(drain), 0, abort_flag, err, kErrWaitDrain);
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kGemmTmemCols);
+  }
+}
+
+}  // namespace moe

@@ -3,6 +3,7 @@
 #include "op_common.cuh"
 #include "grouped_mm.cuh"
 #include "grouped_tc.cuh"
+#include "grouped_wgrad.cuh"
 
 using namespace moe;
 
@@ -26,8 +27,8 @@ moe_status check_shape(const Shape& s) {
   // tiles of the smallest kind, all groups together, are counted in 32 bits
   const int64_t nt = (s.n + 63) / 64, kt = (s.k + 63) / 64;
   const int64_t mt = (s.rows + 63) / 64 + s.G;
-  if (mt * (nt > kt ? nt : kt) >= (int64_t(1) << 31) || nt * kt * s.G >= (int64_t(1) << 31))
-    return fail(MOE_ERR_UNSUPPORTED, "more than 2^31 tiles");
+  if (mt * (nt > kt ? nt : kt) >= (int64_t(1) << 31) || nt * kt * s.G >= (int64_t(1) << 30))
+    return fail(MOE_ERR_UNSUPPORTED, "too many tiles");
   return MOE_OK;
 }
 
@@ -38,14 +39,11 @@ cudaError_t launch_simt(const GroupedSimtArgs& a, int64_t tiles, int n_sms, cuda
                     st, a);
 }
 
-// Clusters of the paired kernel that can be resident at once on the current device (asked for
-// once per device; also sets the kernel's shared-memory limit).
-template <int OP>
-moe_status pair_clusters(int device, int n_sms, int* out) {
-  static std::atomic<int> kept[64];
+// Clusters of `kernel` that can be resident at once on the current device (asked for once per
+// device, which also sets the kernel's shared-memory limit; `kept` is the kernel's own).
+moe_status pair_clusters(const void* kernel, int threads, std::atomic<int>* kept, int device, int n_sms, int* out) {
   if (device < 64 && (*out = kept[device].load(std::memory_order_acquire)) > 0) return MOE_OK;
-  MOE_CUDA(cudaFuncSetAttribute((const void*)grouped_pair_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)kGemmSmemBytes));
+  MOE_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmemBytes));
   cudaLaunchConfig_t lc = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -53,12 +51,12 @@ moe_status pair_clusters(int device, int n_sms, int* out) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   lc.gridDim = dim3(2 * (n_sms / 2), 1, 1);
-  lc.blockDim = dim3(kGpThreads, 1, 1);
+  lc.blockDim = dim3(threads, 1, 1);
   lc.dynamicSmemBytes = kGemmSmemBytes;
   lc.attrs = attr;
   lc.numAttrs = 1;
   int n = 0;
-  MOE_CUDA(cudaOccupancyMaxActiveClusters(&n, (const void*)grouped_pair_kernel<OP>, &lc));
+  MOE_CUDA(cudaOccupancyMaxActiveClusters(&n, kernel, &lc));
   if (n < 1) return fail(MOE_ERR_UNSUPPORTED, "no CTA pair of the grouped product fits on this device");
   if (device < 64) kept[device].store(n, std::memory_order_release);
   *out = n;
@@ -69,27 +67,29 @@ moe_status pair_clusters(int device, int n_sms, int* out) {
 template <int OP>
 moe_status launch_tc(const void* a, const void* b, const int32_t* counts, const Shape& s, int accumulate,
                      void* out, int device, int n_sms, cudaStream_t st) {
+  static std::atomic<int> kept[64];
+  constexpr bool W = OP == kGroupedWgrad;
   CUtensorMap tmA, tmB;
-  bool ok;
-  if (OP == kGroupedMM)
-    ok = encode_2d(&tmA, a, s.k, s.rows, 128) && encode_3d(&tmB, b, s.k, s.n, s.G, 128);
-  else if (OP == kGroupedDgrad)
-    ok = encode_2d(&tmA, a, s.n, s.rows, 128) && encode_3d(&tmB, b, s.k, s.n, s.G, 64);
-  else
-    ok = encode_2d(&tmA, a, s.n, s.rows, 64) && encode_2d(&tmB, b, s.k, s.rows, 64);
+  const bool ok = W ? encode_2d(&tmA, a, s.n, s.rows, 64) && encode_2d(&tmB, b, s.k, s.rows, 64)
+                    : encode_2d(&tmA, a, OP == kGroupedMM ? s.k : s.n, s.rows, 128) &&
+                          encode_3d(&tmB, b, s.k, s.n, s.G, OP == kGroupedMM ? 128 : 64);
   if (!ok) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for a grouped product's operand");
-  int clusters = 0;
-  MOE_TRY(pair_clusters<OP>(device, n_sms, &clusters));
   const int out_cols = OP == kGroupedMM ? s.n : s.k;
   const int64_t nt = (out_cols + kGemmBN - 1) / kGemmBN;
-  const int64_t tiles = OP == kGroupedWgrad
-                            ? s.G * nt * ((s.n + kPairBM - 1) / kPairBM)
-                            : ((s.rows + kPairBM - 1) / kPairBM + (s.G < s.rows ? s.G : s.rows)) * nt;
-  const int out_es = OP == kGroupedWgrad ? 4 : 2;
   GroupedPairArgs p{counts, s.G, (int)s.rows, s.n, s.k, out, accumulate,
-                    !misaligned(out, 32) && (out_cols * out_es) % 32 == 0};
-  MOE_CUDA(launch_pdl(grouped_pair_kernel<OP>, dim3(2 * (unsigned)(tiles < clusters ? tiles : clusters)),
-                      dim3(kGpThreads), kGemmSmemBytes, st, tmA, tmB, p));
+                    !misaligned(out, 32) && (out_cols * (W ? 4 : 2)) % 32 == 0};
+  int clusters = 0;
+  if constexpr (W) {
+    MOE_TRY(pair_clusters((const void*)grouped_wgrad_kernel, kGwThreads, kept, device, n_sms, &clusters));
+    const int64_t tiles = s.G * nt * ((s.n + kPairBM - 1) / kPairBM);   // a cluster each
+    MOE_CUDA(launch_pdl(grouped_wgrad_kernel, dim3(2 * (unsigned)tiles), dim3(kGwThreads), kGemmSmemBytes, st, tmA,
+                        tmB, p));
+  } else {
+    MOE_TRY(pair_clusters((const void*)grouped_pair_kernel<OP>, kGpThreads, kept, device, n_sms, &clusters));
+    const int64_t tiles = ((s.rows + kPairBM - 1) / kPairBM + (s.G < s.rows ? s.G : s.rows)) * nt;
+    MOE_CUDA(launch_pdl(grouped_pair_kernel<OP>, dim3(2 * (unsigned)(tiles < clusters ? tiles : clusters)),
+                        dim3(kGpThreads), kGemmSmemBytes, st, tmA, tmB, p));
+  }
   return MOE_OK;
 }
 
