@@ -4,7 +4,7 @@
 // with cta_group::2 (M = 256), the roles and the ring of gemm_tc.cuh.  The operands are read
 // where they lie, without transposed copies: an operand whose contraction index is contiguous
 // arrives as a K-major tile, one whose output index is contiguous (W of dgrad; dy and x of
-// wgrad) as an MN-major tile -- boxes of 64 output columns x 64 contraction rows, 128-byte
+// wgrad) as an MN-major tile -- boxes of 64 output columns x 128 contraction rows, 128-byte
 // swizzled, which the MMA reads through the descriptor's strides.
 //
 // An expert's last row tile reads on into the next expert's rows; those accumulator rows are
@@ -21,7 +21,11 @@ static __device__ int g_grouped_err;
 
 constexpr int kGpEpiWarps = 8;
 constexpr int kGpThreads = 64 + 32 * kGpEpiWarps;
-constexpr uint32_t kGpBox = 64 * 128;                     // one MN-major box: 64 rows of 128 bytes
+// One MN-major box: the contraction rows of a whole stage (two k-blocks), 128 bytes each.  One
+// load per 64 columns and stage instead of one per k-block: the loads' issue, not their bytes,
+// held the MMA back (weight gradients of 6144 rows an expert: 990 -> 1324 TFLOP/s without them).
+constexpr int kGpBoxRows = kGemmKPS * kGemmBK;
+constexpr uint32_t kGpBox = kGpBoxRows * 128;
 
 struct GroupedPairArgs {
   const int32_t* counts;
@@ -31,7 +35,7 @@ struct GroupedPairArgs {
   int wide;              // output rows are 32-byte aligned: 32-byte stores
 };
 
-// MN-major tile of 64-element blocks, each 64 contraction rows x 128 bytes (128-byte swizzle):
+// MN-major tile of 64-element blocks, each a box of kGpBoxRows rows of 128 bytes (128-byte swizzle):
 // leading offset = distance of two blocks (64 output columns), stride offset = 8 contraction
 // rows.
 __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
@@ -172,18 +176,17 @@ grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
           const uint32_t sa = smem_u32(base + (size_t)stage * kGemmStageBytes);
           const int nk = c.kb - kb0 < kGemmKPS ? c.kb - kb0 : kGemmKPS;
           const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
-          if (leader)
-            mbar_arrive_expect_tx(smem_u32(&full[stage]), 2u * (uint32_t)nk * (kGemmABytes + kGemmBBytes));
+          if (leader)   // both CTAs' bytes
+            mbar_arrive_expect_tx(smem_u32(&full[stage]),
+                                  2u * ((uint32_t)nk * kGemmABytes + (kBMn ? 2u * kGpBox : (uint32_t)nk * kGemmBBytes)));
           for (int j = 0; j < nk; ++j) {
             const int q = (kb0 + j) * kGemmBK;   // contraction index
-            const uint32_t da = sa + j * kGemmABytes, db = sa + kGemmBOff + j * kGemmBBytes;
-            tma_load_2d_pair(da, &tmA, fb, q, a0);
-            if constexpr (!kBMn) {
-              tma_load_3d_pair(db, &tmB, fb, q, b0, c.g);
-            } else {
-              tma_load_3d_pair(db, &tmB, fb, b0, q, c.g);
-              tma_load_3d_pair(db + kGpBox, &tmB, fb, b0 + 64, q, c.g);
-            }
+            tma_load_2d_pair(sa + j * kGemmABytes, &tmA, fb, q, a0);
+            if (!kBMn) tma_load_3d_pair(sa + kGemmBOff + j * kGemmBBytes, &tmB, fb, q, b0, c.g);
+          }
+          if (kBMn) {   // rows behind the contraction's end arrive as zeros
+            tma_load_3d_pair(sa + kGemmBOff, &tmB, fb, b0, kb0 * kGemmBK, c.g);
+            tma_load_3d_pair(sa + kGemmBOff + kGpBox, &tmB, fb, b0 + 64, kb0 * kGemmBK, c.g);
           }
           if (++stage == kGemmStages) { stage = 0; phase ^= 1u; }
         }
@@ -220,9 +223,9 @@ grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
           const uint32_t sa = smem_u32(base + (size_t)stage * kGemmStageBytes);
           const int nk = c.kb - kb0 < kGemmKPS ? c.kb - kb0 : kGemmKPS;
           for (int j = 0; j < nk; ++j) {
-            const uint32_t pa = sa + j * kGemmABytes, pb = sa + kGemmBOff + j * kGemmBBytes;
-            const uint64_t ad = sdesc_k_sw128(pa);
-            const uint64_t bd = kBMn ? sdesc_mn_sw128(pb) : sdesc_k_sw128(pb);
+            const uint64_t ad = sdesc_k_sw128(sa + j * kGemmABytes);
+            const uint64_t bd = kBMn ? sdesc_mn_sw128(sa + kGemmBOff + j * (kGemmBK * 128u))
+                                     : sdesc_k_sw128(sa + kGemmBOff + j * kGemmBBytes);
             // 16 contraction values a step: 32 bytes along a K-major row, 16 rows of 128 bytes
             // of an MN-major box
 #pragma unroll

@@ -3,16 +3,17 @@
 //
 // Clusters of two CTAs, 256 x 256 tiles of dW_e, tcgen05.mma with cta_group::2.  dy and x are read
 // where they lie: their contiguous index is an output index, so both operands are MN-major
-// tiles (boxes of 64 columns x 64 rows).
+// tiles (boxes of 64 columns x 128 rows, one
+// stage of the ring).
 //
 // Precision: the tensor cores truncate when they add to an accumulator, which over n steps of
 // 16 rows leaves a bias of about 2.2e-8 n of the value (measured: 7.4e-6 of dW's norm when an
-// expert had 10,800 rows in one chain).  So a chain is cut after kGwChunk k-blocks of 64
+// expert had 10,800 rows in one chain).  So a chain is cut after kGwChunk stages of 128
 // rows: the epilogue warps add the pieces in registers with round-to-nearest while the MMA
 // fills the other accumulator.
 //
-// Ragged rows: a tile's last k-block runs ceil(t / 16) of its four MMA steps for t rows, and
-// the rows behind t in the last step are zeroed in both operands (0 x NaN would be NaN) by a
+// Ragged rows: a tile's last stage runs ceil(t / 16) of its eight MMA steps for t rows, and the
+// rows behind t in the last step are zeroed in both operands (0 x NaN would be NaN) by a
 // warp of each CTA before the MMA: that stage's loads complete on a barrier of the CTA, and
 // the zeroing warp arrives on the leader's "full" barrier in its stead.
 //
@@ -26,13 +27,13 @@
 
 namespace moe {
 
-constexpr int kGwChunk = 8;                                // k-blocks per accumulator chain
+constexpr int kGwChunk = 4;                                // stages per accumulator chain
 constexpr int kGwThreads = 64 + 32 * (kGpEpiWarps + 1);    // + the zeroing warp
 constexpr int kGwSlots = 4;                                // tiles taken over ahead
 // arrivals that free a slot: in each CTA the producer, the zeroing warp and the epilogue
 // warps, in the leader also the MMA issuer
 constexpr int kGwReaders = 2 * (2 + kGpEpiWarps) + 1;
-static_assert(kGwChunk % kGemmKPS == 0, "a stage belongs to one chain");
+static_assert(4 * kGpBox == kGemmStageBytes && kGemmBOff == 2 * kGpBox, "a stage is two boxes each of A and B");
 
 // The experts' first rows, and the experts in order of falling row counts.
 struct WgradTable {
@@ -148,14 +149,14 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     c.n = local - c.m * nt;
     c.row0 = tab.row0[c.g];
     c.grows = tab.row0[c.g + 1] - c.row0;
-    c.kb = (c.grows + kGemmBK - 1) / kGemmBK;
+    c.kb = (c.grows + kGpBoxRows - 1) / kGpBoxRows;   // stages
     return c;
   };
   auto tile_cols = [&](int n) {   // the MMA's N: a multiple of 32
     const int left = a.K - n * kGemmBN;
     return left >= kGemmBN ? kGemmBN : (left + 31) & ~31;
   };
-  auto tail_rows = [&](const GpTile& c) { return c.grows - (c.kb - 1) * kGemmBK; };
+  auto tail_rows = [&](const GpTile& c) { return c.grows - (c.kb - 1) * kGpBoxRows; };   // of the last stage
   // The next tile (one thread of each reader), or -1: none left, or a wait ran out.
   struct Next {
     int slot = 0;
@@ -189,26 +190,21 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         const GpTile c = tile_of(tile);
         const int a0 = c.m * kPairBM + (int)rank * 128;
         const int b0 = c.n * kGemmBN + (int)rank * (tile_cols(c.n) / 2);
-        for (int kb0 = 0; kb0 < c.kb; kb0 += kGemmKPS) {
+        for (int kb = 0; kb < c.kb; ++kb) {
           ok = mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, err, kErrWaitProducer);
           if (!ok) break;
           const uint32_t sa = smem_u32(base + (size_t)stage * kGemmStageBytes);
-          const int nk = c.kb - kb0 < kGemmKPS ? c.kb - kb0 : kGemmKPS;
-          const uint32_t bytes = (uint32_t)nk * (kGemmABytes + kGemmBBytes);   // this CTA's
-          const bool fix = kb0 + nk == c.kb && (tail_rows(c) & 15) != 0;
+          const bool fix = kb == c.kb - 1 && (tail_rows(c) & 15) != 0;
           const uint32_t fb =
               fix ? mapa_shared(smem_u32(&tail[stage]), rank) : mapa_shared(smem_u32(&full[stage]), 0);
-          if (fix) mbar_arrive_expect_tx(smem_u32(&tail[stage]), bytes);
-          else if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2u * bytes);
+          if (fix) mbar_arrive_expect_tx(smem_u32(&tail[stage]), kGemmStageBytes);
+          else if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2u * kGemmStageBytes);
           else mbar_arrive_cluster(fb);
-          for (int j = 0; j < nk; ++j) {
-            const int row = c.row0 + (kb0 + j) * kGemmBK;
-            const uint32_t da = sa + j * kGemmABytes, db = sa + kGemmBOff + j * kGemmBBytes;
-            tma_load_2d_pair(da, &tmA, fb, a0, row);
-            tma_load_2d_pair(da + kGpBox, &tmA, fb, a0 + 64, row);
-            tma_load_2d_pair(db, &tmB, fb, b0, row);
-            tma_load_2d_pair(db + kGpBox, &tmB, fb, b0 + 64, row);
-          }
+          const int row = c.row0 + kb * kGpBoxRows;
+          tma_load_2d_pair(sa, &tmA, fb, a0, row);
+          tma_load_2d_pair(sa + kGpBox, &tmA, fb, a0 + 64, row);
+          tma_load_2d_pair(sa + kGemmBOff, &tmB, fb, b0, row);
+          tma_load_2d_pair(sa + kGemmBOff + kGpBox, &tmB, fb, b0 + 64, row);
           if (++stage == kGemmStages) { stage = 0; phase ^= 1u; }
         }
         if (ok) tile = next_tile(nx);
@@ -240,21 +236,16 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
           if (!ok) break;
           tc_fence_after();
           const uint32_t dt = tmem_base + static_cast<uint32_t>(acc * kGemmBN);
-          for (int kb0 = kc; kb0 < kend; kb0 += kGemmKPS) {
+          for (int kb = kc; kb < kend; ++kb) {
             ok = mbar_wait_cluster(smem_u32(&full[stage]), phase, abort_flag, err, kErrWaitMma);
             if (!ok) break;
             tc_fence_after();
             const uint32_t sa = smem_u32(base + (size_t)stage * kGemmStageBytes);
-            const int nk = kend - kb0 < kGemmKPS ? kend - kb0 : kGemmKPS;
-            for (int j = 0; j < nk; ++j) {
-              const uint64_t ad = sdesc_mn_sw128(sa + j * kGemmABytes);
-              const uint64_t bd = sdesc_mn_sw128(sa + kGemmBOff + j * kGemmBBytes);
-              // 16 rows of 128 bytes a step
-              const int steps = kb0 + j == c.kb - 1 ? (tail_rows(c) + 15) >> 4 : 4;
+            const uint64_t ad = sdesc_mn_sw128(sa), bd = sdesc_mn_sw128(sa + kGemmBOff);
+            const int steps = kb == c.kb - 1 ? (tail_rows(c) + 15) >> 4 : kGpBoxRows / 16;
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (k < steps) tc_mma_f16_pair(dt, ad + 128u * k, bd + 128u * k, idesc, (kb0 != kc) | j | k);
-            }
+            for (int k = 0; k < kGpBoxRows / 16; ++k)   // 16 rows of 128 bytes a step
+              if (k < steps) tc_mma_f16_pair(dt, ad + 128u * k, bd + 128u * k, idesc, (kb != kc) | k);
             tc_commit_pair_mc(smem_u32(&empty[stage]), 0x3);
             if (++stage == kGemmStages) { stage = 0; phase ^= 1u; }
           }
@@ -272,9 +263,8 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     Next nx;
     for (int tile = first; tile >= 0;) {
       const GpTile c = tile_of(tile);
-      const int stages = (c.kb + kGemmKPS - 1) / kGemmKPS;
-      const int last = (stage + stages + kGemmStages - 1) % kGemmStages;
-      stage = (stage + stages) % kGemmStages;
+      const int last = (stage + c.kb + kGemmStages - 1) % kGemmStages;
+      stage = (stage + c.kb) % kGemmStages;
       const int t = tail_rows(c);
       if (c.kb > 0 && (t & 15) != 0) {
         int ok = 1;
@@ -282,17 +272,13 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
         __syncwarp();
         tail_phase ^= 1u << last;
-        // rows [t, 16 ceil(t / 16)) of the stage's last k-block: two boxes each of A and B, 128
-        // bytes a row (the swizzle permutes 16-byte chunks within a row)
+        // rows [t, 16 ceil(t / 16)) of the stage's four boxes, 128 bytes a row (the swizzle
+        // permutes 16-byte chunks within a row)
         uint8_t* sp = base + (size_t)last * kGemmStageBytes;
-        const int j = (c.kb - 1) % kGemmKPS;
         const int nz = ((t + 15) & ~15) - t;
-        for (int i = lane; i < nz * 32; i += 32) {
-          const int row = t + (i >> 5), box = (i >> 3) & 3, chunk = i & 7;
-          uint8_t* p = sp + (box < 2 ? j * kGemmABytes : kGemmBOff + j * kGemmBBytes) + (box & 1) * kGpBox +
-                       row * 128 + chunk * 16;
-          *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int i = lane; i < nz * 32; i += 32)
+          *reinterpret_cast<uint4*>(sp + ((i >> 3) & 3) * kGpBox + (t + (i >> 5)) * 128 + (i & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_shared();   // the zeros, before the tensor cores read the stage
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[last]), 0));

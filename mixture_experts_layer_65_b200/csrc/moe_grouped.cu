@@ -70,9 +70,9 @@ moe_status launch_tc(const void* a, const void* b, const int32_t* counts, const 
   static std::atomic<int> kept[64];
   constexpr bool W = OP == kGroupedWgrad;
   CUtensorMap tmA, tmB;
-  const bool ok = W ? encode_2d(&tmA, a, s.n, s.rows, 64) && encode_2d(&tmB, b, s.k, s.rows, 64)
+  const bool ok = W ? encode_2d(&tmA, a, s.n, s.rows, kGpBoxRows) && encode_2d(&tmB, b, s.k, s.rows, kGpBoxRows)
                     : encode_2d(&tmA, a, OP == kGroupedMM ? s.k : s.n, s.rows, 128) &&
-                          encode_3d(&tmB, b, s.k, s.n, s.G, OP == kGroupedMM ? 128 : 64);
+                          encode_3d(&tmB, b, s.k, s.n, s.G, 128);
   if (!ok) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for a grouped product's operand");
   const int out_cols = OP == kGroupedMM ? s.n : s.k;
   const int64_t nt = (out_cols + kGemmBN - 1) / kGemmBN;
