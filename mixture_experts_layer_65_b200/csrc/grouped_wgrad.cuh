@@ -15,12 +15,20 @@
 // Ragged rows: a tile's last stage runs ceil(t / 16) of its eight MMA steps for t rows, and the
 // rows behind t in the last step are zeroed in both operands (0 x NaN would be NaN) by a
 // warp of each CTA before the MMA: that stage's loads complete on a barrier of the CTA, and
-// the zeroing warp arrives on the leader's "full" barrier in its stead.
+// the leader's zeroing warp, told by the peer's, arrives on the "full" barrier instead of the
+// producer.  (A second arrival, by the peer's producer, on every stage's "full" barrier held
+// the kernel to 1195 TFLOP/s instead of 1412 with 65,536 rows in one expert: its release at
+// cluster scope waits for the thread's earlier work.)
 //
 // Balance: a tile's time goes with its expert's rows, which may differ a hundredfold.  The
 // grid has one cluster per tile, experts with most rows first; a running cluster takes the
 // next unstarted one over (clusterlaunchcontrol), so no cluster is left with a long tile at
 // the end, and which cluster computes a tile does not change its value.
+//
+// Output: each epilogue warp passes its 32 rows through shared memory, 16 columns (64-byte
+// swizzled rows of 64 bytes) at a time, to TMA stores, which cut off what lies outside dW; an
+// accumulating call makes them reductions (one addition per element, rounded to nearest;
+// subnormal sums become 0), so nothing is read back.
 #pragma once
 
 #include "grouped_tc.cuh"
@@ -29,7 +37,11 @@ namespace moe {
 
 constexpr int kGwChunk = 4;                                // stages per accumulator chain
 constexpr int kGwThreads = 64 + 32 * (kGpEpiWarps + 1);    // + the zeroing warp
-constexpr int kGwSlots = 4;                                // tiles taken over ahead
+constexpr int kGwSlots = 4;                                // answers about tiles to take over
+constexpr int kGwAhead = 2;                                // requests made ahead
+constexpr int kGwStoreCols = 16;
+constexpr uint32_t kGwStoreBytes = 32 * kGwStoreCols * 4;  // one epilogue warp's staging
+constexpr size_t kGwSmemBytes = kGemmSmemBytes + 1024 + kGpEpiWarps * kGwStoreBytes;
 // arrivals that free a slot: in each CTA the producer, the zeroing warp and the epilogue
 // warps, in the leader also the MMA issuer
 constexpr int kGwReaders = 2 * (2 + kGpEpiWarps) + 1;
@@ -72,9 +84,29 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_a
                : "memory");
 }
 
+// Store (or add) a box from shared memory; the part of it outside the tensor is left out.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t c0, int32_t c1,
+                                             int32_t c2, bool add) {
+  if (add)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All of this thread's stores: their shared memory read (so that it can be written again), or
+// their results written.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 static __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGwThreads, 1)
 grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     GroupedPairArgs a) {
+                     const __grid_constant__ CUtensorMap tmOut, GroupedPairArgs a) {
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   __shared__ WgradTable tab;
@@ -88,10 +120,12 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   uint64_t* acc_empty = acc_full + 2;                   // used in the leader
   uint64_t* drain = acc_empty + 2;                      // both CTAs
   uint64_t* tail = drain + 1;                           // both CTAs: loads of a tail stage
-  uint64_t* next_full = tail + kGemmStages;             // both CTAs: an answer has arrived
+  uint64_t* peer_tail = tail + kGemmStages;             // used in the leader: the peer's zeros
+  uint64_t* next_full = peer_tail + kGemmStages;        // both CTAs: an answer has arrived
   uint64_t* next_empty = next_full + kGwSlots;          // used in the leader: all have read it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(next_empty + kGwSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint8_t* store_base = ctl + 1024;   // 1024-byte aligned, as the swizzle wants
   int* err = &g_grouped_err;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -100,7 +134,8 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kGemmStages; ++s) {
-      mbar_init(smem_u32(&full[s]), 2);    // each CTA's producer, or its zeroing warp
+      mbar_init(smem_u32(&full[s]), 1);    // the leader's producer, or its zeroing warp
+      mbar_init(smem_u32(&peer_tail[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
       mbar_init(smem_u32(&tail[s]), 1);
     }
@@ -117,6 +152,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmOut);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), kGemmTmemCols);
@@ -178,15 +214,17 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      Next nx;
+      Next nx, ask;
+      auto request = [&] {   // (leader) ask for one more tile
+        ok = mbar_wait_cluster(smem_u32(&next_empty[ask.slot]), ask.phase ^ 1u, abort_flag, err, kErrWaitProducer);
+        if (!ok) return;
+        mbar_arrive_expect_tx(smem_u32(&next_full[ask.slot]), 16);
+        mbar_arrive_expect_tx_cluster(mapa_shared(smem_u32(&next_full[ask.slot]), 1), 16);
+        clc_try_cancel(smem_u32(answers[ask.slot]), smem_u32(&next_full[ask.slot]));
+        if (++ask.slot == kGwSlots) { ask.slot = 0; ask.phase ^= 1u; }
+      };
+      for (int i = 0; i < kGwAhead && leader && ok; ++i) request();
       for (int tile = first; tile >= 0 && ok;) {
-        if (leader) {   // ask for the tile after this one
-          ok = mbar_wait_cluster(smem_u32(&next_empty[nx.slot]), nx.phase ^ 1u, abort_flag, err, kErrWaitProducer);
-          if (!ok) break;
-          mbar_arrive_expect_tx(smem_u32(&next_full[nx.slot]), 16);
-          mbar_arrive_expect_tx_cluster(mapa_shared(smem_u32(&next_full[nx.slot]), 1), 16);
-          clc_try_cancel(smem_u32(answers[nx.slot]), smem_u32(&next_full[nx.slot]));
-        }
         const GpTile c = tile_of(tile);
         const int a0 = c.m * kPairBM + (int)rank * 128;
         const int b0 = c.n * kGemmBN + (int)rank * (tile_cols(c.n) / 2);
@@ -199,7 +237,6 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
               fix ? mapa_shared(smem_u32(&tail[stage]), rank) : mapa_shared(smem_u32(&full[stage]), 0);
           if (fix) mbar_arrive_expect_tx(smem_u32(&tail[stage]), kGemmStageBytes);
           else if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2u * kGemmStageBytes);
-          else mbar_arrive_cluster(fb);
           const int row = c.row0 + kb * kGpBoxRows;
           tma_load_2d_pair(sa, &tmA, fb, a0, row);
           tma_load_2d_pair(sa + kGpBox, &tmA, fb, a0 + 64, row);
@@ -207,7 +244,14 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
           tma_load_2d_pair(sa + kGemmBOff + kGpBox, &tmB, fb, b0 + 64, row);
           if (++stage == kGemmStages) { stage = 0; phase ^= 1u; }
         }
-        if (ok) tile = next_tile(nx);
+        if (!ok) break;
+        tile = next_tile(nx);
+        if (tile >= 0 && leader) request();
+      }
+      // the answers to the requests that were still open when none was left
+      for (int i = 1; i < kGwAhead && ok; ++i) {
+        ok = mbar_wait_cluster(smem_u32(&next_full[nx.slot]), nx.phase, abort_flag, err, kErrWaitDrain);
+        if (++nx.slot == kGwSlots) { nx.slot = 0; nx.phase ^= 1u; }
       }
       if (!ok) {   // gave up: let the copies in flight land before the CTA's memory is handed on
         const uint64_t t0 = globaltimer_ns();
@@ -237,7 +281,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
           tc_fence_after();
           const uint32_t dt = tmem_base + static_cast<uint32_t>(acc * kGemmBN);
           for (int kb = kc; kb < kend; ++kb) {
-            ok = mbar_wait_cluster(smem_u32(&full[stage]), phase, abort_flag, err, kErrWaitMma);
+            ok = mbar_wait(smem_u32(&full[stage]), phase, abort_flag, err, kErrWaitMma);
             if (!ok) break;
             tc_fence_after();
             const uint32_t sa = smem_u32(base + (size_t)stage * kGemmStageBytes);
@@ -271,7 +315,6 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         if (lane == 0) ok = mbar_wait(smem_u32(&tail[last]), tail_phase >> last & 1u, abort_flag, err, kErrWaitDrain);
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
         __syncwarp();
-        tail_phase ^= 1u << last;
         // rows [t, 16 ceil(t / 16)) of the stage's four boxes, 128 bytes a row (the swizzle
         // permutes 16-byte chunks within a row)
         uint8_t* sp = base + (size_t)last * kGemmStageBytes;
@@ -281,7 +324,16 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
               make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_shared();   // the zeros, before the tensor cores read the stage
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[last]), 0));
+        if (lane == 0) {
+          if (!leader) {
+            mbar_arrive_cluster(mapa_shared(smem_u32(&peer_tail[last]), 0));
+          } else {
+            ok = mbar_wait_cluster(smem_u32(&peer_tail[last]), tail_phase >> last & 1u, abort_flag, err, kErrWaitDrain);
+            if (ok) mbar_arrive(smem_u32(&full[last]));
+          }
+        }
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        tail_phase ^= 1u << last;
       }
       if (lane == 0) tile = next_tile(nx);
       tile = __shfl_sync(0xffffffffu, tile, 0);
@@ -290,7 +342,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     // ------------------------------------------------------------------ epilogue
     const int q = warp & 3;                 // TMEM lane quadrant
     const int half = (warp - 2) >> 2;       // which half of the tile's columns
-    const int rr = q * 32 + lane;
+    uint8_t* stage_out = store_base + (warp - 2) * kGwStoreBytes;
     int it = 0;
     Next nx;
     for (int tile = first; tile >= 0;) {
@@ -333,28 +385,25 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[acc]), 0));
       }
       if (!ok) break;
-      const int mrow = c.m * kPairBM + (int)rank * 128 + rr;
-      if (mrow < a.N && !(c.kb == 0 && a.accumulate)) {
+      const int mrow0 = c.m * kPairBM + (int)rank * 128 + q * 32;   // first of this warp's rows
+      if (mrow0 < a.N && !(c.kb == 0 && a.accumulate)) {
         const int col0 = c.n * kGemmBN + half * (kGemmBN / 2);
-        float* o = static_cast<float*>(a.out) + ((size_t)c.g * a.N + mrow) * a.K + col0;
-        const int left = a.K - col0;   // a multiple of 8
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          if (8 * x >= left) break;
-          uint32_t* v = &s[x >> 2][(x & 3) * 8];
-          if (a.accumulate) {
-            const float4 p0 = *reinterpret_cast<const float4*>(o + 8 * x);
-            const float4 p1 = *reinterpret_cast<const float4*>(o + 8 * x + 4);
-            const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+        for (int x = 0; x < kGemmBN / 2 / kGwStoreCols; ++x) {
+          if (col0 + x * kGwStoreCols >= a.K) break;
+          if (lane == 0) bulk_wait_read();
+          __syncwarp();
+          // 16-byte chunk i of this row's 64 bytes at i ^ (row / 2 % 4)
+          const uint32_t* v = &s[x >> 1][(x & 1) * kGwStoreCols];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(p[i] + __uint_as_float(v[i]));
-          }
-          const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
-          if (a.wide) {
-            st_global_v8(o + 8 * x, lo, hi);
-          } else {
-            *reinterpret_cast<uint4*>(o + 8 * x) = lo;
-            *reinterpret_cast<uint4*>(o + 8 * x + 4) = hi;
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(stage_out + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tmOut, smem_u32(stage_out), col0 + x * kGwStoreCols, mrow0, c.g, a.accumulate);
+            bulk_commit();
           }
         }
       }
@@ -362,6 +411,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
       if (lane == 0) tile = next_tile(nx);
       tile = __shfl_sync(0xffffffffu, tile, 0);
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   // teardown: all MMAs of the pair have completed before TMEM is released in either CTA

@@ -41,9 +41,10 @@ cudaError_t launch_simt(const GroupedSimtArgs& a, int64_t tiles, int n_sms, cuda
 
 // Clusters of `kernel` that can be resident at once on the current device (asked for once per
 // device, which also sets the kernel's shared-memory limit; `kept` is the kernel's own).
-moe_status pair_clusters(const void* kernel, int threads, std::atomic<int>* kept, int device, int n_sms, int* out) {
+moe_status pair_clusters(const void* kernel, int threads, size_t smem, std::atomic<int>* kept, int device, int n_sms,
+                         int* out) {
   if (device < 64 && (*out = kept[device].load(std::memory_order_acquire)) > 0) return MOE_OK;
-  MOE_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmemBytes));
+  MOE_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
   cudaLaunchConfig_t lc = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -52,7 +53,7 @@ moe_status pair_clusters(const void* kernel, int threads, std::atomic<int>* kept
   attr[0].val.clusterDim.z = 1;
   lc.gridDim = dim3(2 * (n_sms / 2), 1, 1);
   lc.blockDim = dim3(threads, 1, 1);
-  lc.dynamicSmemBytes = kGemmSmemBytes;
+  lc.dynamicSmemBytes = smem;
   lc.attrs = attr;
   lc.numAttrs = 1;
   int n = 0;
@@ -61,6 +62,20 @@ moe_status pair_clusters(const void* kernel, int threads, std::atomic<int>* kept
   if (device < 64) kept[device].store(n, std::memory_order_release);
   *out = n;
   return MOE_OK;
+}
+
+// fp32 [depth, outer, inner], boxes of 32 rows x 16 values (64 bytes, 64-byte swizzle): the
+// weight gradients' stores.
+bool encode_out_f32(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t depth) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {inner, outer, depth};
+  cuuint64_t strides[2] = {inner * 4, inner * outer * 4};
+  cuuint32_t box[3] = {kGwStoreCols, 32, 1};
+  cuuint32_t ess[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(ptr), dims, strides, box, ess,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The products on the tensor cores: bf16, widths in whole 16-byte vectors, aligned buffers.
@@ -80,12 +95,15 @@ moe_status launch_tc(const void* a, const void* b, const int32_t* counts, const 
                     !misaligned(out, 32) && (out_cols * (W ? 4 : 2)) % 32 == 0};
   int clusters = 0;
   if constexpr (W) {
-    MOE_TRY(pair_clusters((const void*)grouped_wgrad_kernel, kGwThreads, kept, device, n_sms, &clusters));
+    CUtensorMap tmOut;
+    if (!encode_out_f32(&tmOut, out, s.k, s.n, s.G))
+      return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the weight gradients");
+    MOE_TRY(pair_clusters((const void*)grouped_wgrad_kernel, kGwThreads, kGwSmemBytes, kept, device, n_sms, &clusters));
     const int64_t tiles = s.G * nt * ((s.n + kPairBM - 1) / kPairBM);   // a cluster each
-    MOE_CUDA(launch_pdl(grouped_wgrad_kernel, dim3(2 * (unsigned)tiles), dim3(kGwThreads), kGemmSmemBytes, st, tmA,
-                        tmB, p));
+    MOE_CUDA(launch_pdl(grouped_wgrad_kernel, dim3(2 * (unsigned)tiles), dim3(kGwThreads), kGwSmemBytes, st, tmA,
+                        tmB, tmOut, p));
   } else {
-    MOE_TRY(pair_clusters((const void*)grouped_pair_kernel<OP>, kGpThreads, kept, device, n_sms, &clusters));
+    MOE_TRY(pair_clusters((const void*)grouped_pair_kernel<OP>, kGpThreads, kGemmSmemBytes, kept, device, n_sms, &clusters));
     const int64_t tiles = ((s.rows + kPairBM - 1) / kPairBM + (s.G < s.rows ? s.G : s.rows)) * nt;
     MOE_CUDA(launch_pdl(grouped_pair_kernel<OP>, dim3(2 * (unsigned)(tiles < clusters ? tiles : clusters)),
                         dim3(kGpThreads), kGemmSmemBytes, st, tmA, tmB, p));
