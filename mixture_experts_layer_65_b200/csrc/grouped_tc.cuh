@@ -35,11 +35,11 @@ struct GroupedPairArgs {
   int wide;              // output rows are 32-byte aligned: 32-byte stores
 };
 
-// MN-major tile of 64-element blocks, each a box of kGpBoxRows rows of 128 bytes (128-byte swizzle):
-// leading offset = distance of two blocks (64 output columns), stride offset = 8 contraction
+// MN-major tile of 64-element blocks, each a box of rows of 128 bytes (128-byte swizzle): leading
+// offset = distance of two blocks (64 output columns: a box), stride offset = 8 contraction
 // rows.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(kGpBox >> 4) << 16) |
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t box) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(box >> 4) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
          (static_cast<uint64_t>(2) << 61);
 }
@@ -224,7 +224,7 @@ grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
           const int nk = c.kb - kb0 < kGemmKPS ? c.kb - kb0 : kGemmKPS;
           for (int j = 0; j < nk; ++j) {
             const uint64_t ad = sdesc_k_sw128(sa + j * kGemmABytes);
-            const uint64_t bd = kBMn ? sdesc_mn_sw128(sa + kGemmBOff + j * (kGemmBK * 128u))
+            const uint64_t bd = kBMn ? sdesc_mn_sw128(sa + kGemmBOff + j * (kGemmBK * 128u), kGpBox)
                                      : sdesc_k_sw128(sa + kGemmBOff + j * kGemmBBytes);
             // 16 contraction values a step: 32 bytes along a K-major row, 16 rows of 128 bytes
             // of an MN-major box
@@ -259,36 +259,38 @@ grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
       const int mrow = c.m * kPairBM + (int)rank * 128 + rr;   // row of the expert
       const bool row_ok = mrow < c.grows;
       const size_t orow = (size_t)c.row0 + mrow;
-#pragma unroll 1
-      for (int cc = half * (kGemmBN / 2); cc < (half + 1) * (kGemmBN / 2); cc += 32) {
-        const int col = c.n * kGemmBN + cc;
-        if (col >= out_cols) break;
+      // this thread's half row, rounded, in registers: the accumulator is free before the
+      // stores (whose completion a release behind them would wait for)
+      const int col0 = c.n * kGemmBN + half * (kGemmBN / 2);
+      uint32_t pk[4][16];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (col0 + 32 * x >= out_cols) break;
         uint32_t v[32];
-        __syncwarp();
-        tmem_ld32(trow + static_cast<uint32_t>(cc), v);
+        tmem_ld32(trow + static_cast<uint32_t>(half * (kGemmBN / 2) + 32 * x), v);
         tmem_ld_wait(v);
-        if (!row_ok) continue;
-        const int left = out_cols - col;   // a multiple of 8
-        uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + orow * out_cols + col;
-        if (a.wide && left >= 32) {
-          st_global_v8(o, make_uint4(pk[0], pk[1], pk[2], pk[3]), make_uint4(pk[4], pk[5], pk[6], pk[7]));
-          st_global_v8(o + 16, make_uint4(pk[8], pk[9], pk[10], pk[11]),
-                       make_uint4(pk[12], pk[13], pk[14], pk[15]));
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (8 * x < left)
-              *reinterpret_cast<uint4*>(o + 8 * x) =
-                  make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
-        }
+          pk[x][i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[acc]), 0));
+      if (!row_ok) continue;
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + orow * out_cols + col0;
+      const int left = out_cols - col0;   // a multiple of 8
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        if (16 * x >= left) break;
+        const uint32_t* p = &pk[x >> 1][(x & 1) * 8];
+        const uint4 lo = make_uint4(p[0], p[1], p[2], p[3]), hi = make_uint4(p[4], p[5], p[6], p[7]);
+        if (a.wide) {
+          st_global_v8(o + 16 * x, lo, hi);
+        } else {
+          *reinterpret_cast<uint4*>(o + 16 * x) = lo;
+          if (16 * x + 8 < left) *reinterpret_cast<uint4*>(o + 16 * x + 8) = hi;
+        }
+      }
     }
   }
 

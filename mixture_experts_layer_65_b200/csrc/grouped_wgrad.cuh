@@ -3,16 +3,15 @@
 //
 // Clusters of two CTAs, 256 x 256 tiles of dW_e, tcgen05.mma with cta_group::2.  dy and x are read
 // where they lie: their contiguous index is an output index, so both operands are MN-major
-// tiles (boxes of 64 columns x 128 rows, one
-// stage of the ring).
+// tiles (boxes of 64 columns x 112 rows).
 //
 // Precision: the tensor cores truncate when they add to an accumulator, which over n steps of
 // 16 rows leaves a bias of about 2.2e-8 n of the value (measured: 7.4e-6 of dW's norm when an
-// expert had 10,800 rows in one chain).  So a chain is cut after kGwChunk stages of 128
+// expert had 10,800 rows in one chain).  So a chain is cut after kGwChunk stages of 112
 // rows: the epilogue warps add the pieces in registers with round-to-nearest while the MMA
 // fills the other accumulator.
 //
-// Ragged rows: a tile's last stage runs ceil(t / 16) of its eight MMA steps for t rows, and the
+// Ragged rows: a tile's last stage runs ceil(t / 16) of its seven MMA steps for t rows, and the
 // rows behind t in the last step are zeroed in both operands (0 x NaN would be NaN) by a
 // warp of each CTA before the MMA: that stage's loads complete on a barrier of the CTA, and
 // the leader's zeroing warp, told by the peer's, arrives on the "full" barrier instead of the
@@ -23,10 +22,12 @@
 // Balance: a tile's time goes with its expert's rows, which may differ a hundredfold.  The
 // grid has one cluster per tile, experts with most rows first; a running cluster takes the
 // next unstarted one over (clusterlaunchcontrol), so no cluster is left with a long tile at
-// the end, and which cluster computes a tile does not change its value.
+// the end, and which cluster computes a tile does not change its value.  The leader's producer
+// asks, both CTAs' producers read the answer and hand the tile on to their CTA's warps.
 //
-// Output: each epilogue warp passes its 32 rows through shared memory, 16 columns (64-byte
-// swizzled rows of 64 bytes) at a time, to TMA stores, which cut off what lies outside dW; an
+// Output: each epilogue warp passes its 32 rows through shared memory, 32 columns at a
+// time (128-byte swizzled rows; with rows of 64 bytes the TMA unit's requests bounded the
+// kernel: 141 us instead of XX for 738 MB of zeros), to TMA stores, which cut off what lies outside dW; an
 // accumulating call makes them reductions (one addition per element, rounded to nearest;
 // subnormal sums become 0), so nothing is read back.
 #pragma once
@@ -35,17 +36,20 @@
 
 namespace moe {
 
+// A stage: 112 rows (seven MMA steps), two boxes of 64 columns each of dy and x; what is left of
+// the shared memory beside three of them holds the stores' staging.
+constexpr int kGwRows = 112;
+constexpr int kGwStages = 3;
+constexpr uint32_t kGwBox = kGwRows * 128;
+constexpr uint32_t kGwStageBytes = 4 * kGwBox;
 constexpr int kGwChunk = 4;                                // stages per accumulator chain
 constexpr int kGwThreads = 64 + 32 * (kGpEpiWarps + 1);    // + the zeroing warp
-constexpr int kGwSlots = 4;                                // answers about tiles to take over
+constexpr int kGwSlots = 4;                                // answers, and tiles handed on
 constexpr int kGwAhead = 2;                                // requests made ahead
-constexpr int kGwStoreCols = 16;
+constexpr int kGwStoreCols = 32;
 constexpr uint32_t kGwStoreBytes = 32 * kGwStoreCols * 4;  // one epilogue warp's staging
-constexpr size_t kGwSmemBytes = kGemmSmemBytes + 1024 + kGpEpiWarps * kGwStoreBytes;
-// arrivals that free a slot: in each CTA the producer, the zeroing warp and the epilogue
-// warps, in the leader also the MMA issuer
-constexpr int kGwReaders = 2 * (2 + kGpEpiWarps) + 1;
-static_assert(4 * kGpBox == kGemmStageBytes && kGemmBOff == 2 * kGpBox, "a stage is two boxes each of A and B");
+constexpr size_t kGwSmemBytes = 1024 + kGwStages * kGwStageBytes + 1024 + kGpEpiWarps * kGwStoreBytes;
+static_assert(kGwBox % 1024 == 0 && kGwRows % 16 == 0, "swizzle atoms, MMA steps");
 
 // The experts' first rows, and the experts in order of falling row counts.
 struct WgradTable {
@@ -78,8 +82,10 @@ __device__ __forceinline__ int clc_answer(uint32_t answer) {
   return ok ? static_cast<int>(x) : -1;
 }
 
-__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
+// Arrive on the peer's barrier without ordering anything (it guards only what the barrier
+// itself counts).
+__device__ __forceinline__ void mbar_arrive_expect_tx_peer(uint32_t cluster_addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
                "r"(bytes)
                : "memory");
 }
@@ -99,8 +105,8 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
                  : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// All of this thread's stores: their shared memory read (so that it can be written again), or
-// their results written.
+// All of this thread's stores: their shared memory has been read (and can be written again), or
+// their results are written.
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
@@ -111,19 +117,22 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   extern __shared__ uint8_t smem_raw[];
   __shared__ WgradTable tab;
   __shared__ __align__(16) uint8_t answers[kGwSlots][16];
+  __shared__ volatile int tiles[kGwSlots];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* ctl = base + (size_t)kGemmStages * kGemmStageBytes;
+  uint8_t* ctl = base + (size_t)kGwStages * kGwStageBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctl);   // used in the leader
-  uint64_t* empty = full + kGemmStages;                 // both CTAs
-  uint64_t* acc_full = empty + kGemmStages;             // both CTAs
+  uint64_t* empty = full + kGwStages;                 // both CTAs
+  uint64_t* acc_full = empty + kGwStages;             // both CTAs
   uint64_t* acc_empty = acc_full + 2;                   // used in the leader
   uint64_t* drain = acc_empty + 2;                      // both CTAs
   uint64_t* tail = drain + 1;                           // both CTAs: loads of a tail stage
-  uint64_t* peer_tail = tail + kGemmStages;             // used in the leader: the peer's zeros
-  uint64_t* next_full = peer_tail + kGemmStages;        // both CTAs: an answer has arrived
-  uint64_t* next_empty = next_full + kGwSlots;          // used in the leader: all have read it
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(next_empty + kGwSlots);
+  uint64_t* peer_tail = tail + kGwStages;             // used in the leader: the peer's zeros
+  uint64_t* next_full = peer_tail + kGwStages;        // both CTAs: an answer has arrived
+  uint64_t* next_empty = next_full + kGwSlots;          // used in the leader: the peer has read it
+  uint64_t* tile_full = next_empty + kGwSlots;          // both CTAs: tiles[] filled, and read by all
+  uint64_t* tile_empty = tile_full + kGwSlots;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tile_empty + kGwSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t* store_base = ctl + 1024;   // 1024-byte aligned, as the swizzle wants
   int* err = &g_grouped_err;
@@ -133,7 +142,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   const bool leader = rank == 0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kGemmStages; ++s) {
+    for (int s = 0; s < kGwStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);    // the leader's producer, or its zeroing warp
       mbar_init(smem_u32(&peer_tail[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
@@ -145,7 +154,10 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     }
     for (int s = 0; s < kGwSlots; ++s) {
       mbar_init(smem_u32(&next_full[s]), 1);
-      mbar_init(smem_u32(&next_empty[s]), kGwReaders);
+      mbar_init(smem_u32(&next_empty[s]), 1);
+      mbar_init(smem_u32(&tile_full[s]), 1);
+      // the zeroing warp, the epilogue warps and, in the leader, the MMA issuer
+      mbar_init(smem_u32(&tile_empty[s]), 1 + kGpEpiWarps + (leader ? 1 : 0));
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
@@ -185,26 +197,28 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     c.n = local - c.m * nt;
     c.row0 = tab.row0[c.g];
     c.grows = tab.row0[c.g + 1] - c.row0;
-    c.kb = (c.grows + kGpBoxRows - 1) / kGpBoxRows;   // stages
+    c.kb = (c.grows + kGwRows - 1) / kGwRows;   // stages
     return c;
   };
   auto tile_cols = [&](int n) {   // the MMA's N: a multiple of 32
     const int left = a.K - n * kGemmBN;
     return left >= kGemmBN ? kGemmBN : (left + 31) & ~31;
   };
-  auto tail_rows = [&](const GpTile& c) { return c.grows - (c.kb - 1) * kGpBoxRows; };   // of the last stage
-  // The next tile (one thread of each reader), or -1: none left, or a wait ran out.
-  struct Next {
-    int slot = 0;
+  auto tail_rows = [&](const GpTile& c) { return c.grows - (c.kb - 1) * kGwRows; };   // of the last stage
+  struct Slot {
+    int i = 0;
     uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+      if (++i == kGwSlots) { i = 0; phase ^= 1u; }
+    }
   };
-  auto next_tile = [&](Next& nx) {
-    if (!mbar_wait_cluster(smem_u32(&next_full[nx.slot]), nx.phase, abort_flag, err, kErrWaitProducer)) return -1;
-    const int cta = clc_answer(smem_u32(answers[nx.slot]));
-    fence_proxy_async_shared();   // read before the next answer is written
-    mbar_arrive_cluster(mapa_shared(smem_u32(&next_empty[nx.slot]), 0));
-    if (++nx.slot == kGwSlots) { nx.slot = 0; nx.phase ^= 1u; }
-    return cta < 0 ? -1 : cta >> 1;
+  // The tile the producer hands on (one thread of each reader); -1: none left, or a wait ran out.
+  auto next_tile = [&](Slot& sl) {
+    if (!mbar_wait(smem_u32(&tile_full[sl.i]), sl.phase, abort_flag, err, kErrWaitProducer)) return -1;
+    const int tile = tiles[sl.i];
+    mbar_arrive(smem_u32(&tile_empty[sl.i]));
+    sl.next();
+    return tile;
   };
 
   const int first = blockIdx.x >> 1;
@@ -214,14 +228,23 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      Next nx, ask;
+      Slot ask, got, out;
       auto request = [&] {   // (leader) ask for one more tile
-        ok = mbar_wait_cluster(smem_u32(&next_empty[ask.slot]), ask.phase ^ 1u, abort_flag, err, kErrWaitProducer);
+        ok = mbar_wait_cluster(smem_u32(&next_empty[ask.i]), ask.phase ^ 1u, abort_flag, err, kErrWaitProducer);
         if (!ok) return;
-        mbar_arrive_expect_tx(smem_u32(&next_full[ask.slot]), 16);
-        mbar_arrive_expect_tx_cluster(mapa_shared(smem_u32(&next_full[ask.slot]), 1), 16);
-        clc_try_cancel(smem_u32(answers[ask.slot]), smem_u32(&next_full[ask.slot]));
-        if (++ask.slot == kGwSlots) { ask.slot = 0; ask.phase ^= 1u; }
+        mbar_arrive_expect_tx(smem_u32(&next_full[ask.i]), 16);
+        mbar_arrive_expect_tx_peer(mapa_shared(smem_u32(&next_full[ask.i]), 1), 16);
+        clc_try_cancel(smem_u32(answers[ask.i]), smem_u32(&next_full[ask.i]));
+        ask.next();
+      };
+      auto answer = [&] {   // the next answer: a tile or -1
+        ok = mbar_wait_cluster(smem_u32(&next_full[got.i]), got.phase, abort_flag, err, kErrWaitProducer);
+        if (!ok) return -1;
+        const int cta = clc_answer(smem_u32(answers[got.i]));
+        fence_proxy_async_shared();   // read before the next answer is written
+        if (!leader) mbar_arrive_cluster(mapa_shared(smem_u32(&next_empty[got.i]), 0));
+        got.next();
+        return cta < 0 ? -1 : cta >> 1;
       };
       for (int i = 0; i < kGwAhead && leader && ok; ++i) request();
       for (int tile = first; tile >= 0 && ok;) {
@@ -231,35 +254,38 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         for (int kb = 0; kb < c.kb; ++kb) {
           ok = mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, err, kErrWaitProducer);
           if (!ok) break;
-          const uint32_t sa = smem_u32(base + (size_t)stage * kGemmStageBytes);
+          const uint32_t sa = smem_u32(base + (size_t)stage * kGwStageBytes);
           const bool fix = kb == c.kb - 1 && (tail_rows(c) & 15) != 0;
           const uint32_t fb =
               fix ? mapa_shared(smem_u32(&tail[stage]), rank) : mapa_shared(smem_u32(&full[stage]), 0);
-          if (fix) mbar_arrive_expect_tx(smem_u32(&tail[stage]), kGemmStageBytes);
-          else if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2u * kGemmStageBytes);
-          const int row = c.row0 + kb * kGpBoxRows;
+          if (fix) mbar_arrive_expect_tx(smem_u32(&tail[stage]), kGwStageBytes);
+          else if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2u * kGwStageBytes);
+          const int row = c.row0 + kb * kGwRows;
           tma_load_2d_pair(sa, &tmA, fb, a0, row);
-          tma_load_2d_pair(sa + kGpBox, &tmA, fb, a0 + 64, row);
-          tma_load_2d_pair(sa + kGemmBOff, &tmB, fb, b0, row);
-          tma_load_2d_pair(sa + kGemmBOff + kGpBox, &tmB, fb, b0 + 64, row);
-          if (++stage == kGemmStages) { stage = 0; phase ^= 1u; }
+          tma_load_2d_pair(sa + kGwBox, &tmA, fb, a0 + 64, row);
+          tma_load_2d_pair(sa + 2 * kGwBox, &tmB, fb, b0, row);
+          tma_load_2d_pair(sa + 2 * kGwBox + kGwBox, &tmB, fb, b0 + 64, row);
+          if (++stage == kGwStages) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        tile = next_tile(nx);
+        tile = answer();
         if (tile >= 0 && leader) request();
+        if (!ok) break;
+        ok = mbar_wait(smem_u32(&tile_empty[out.i]), out.phase ^ 1u, abort_flag, err, kErrWaitProducer);
+        if (!ok) break;
+        tiles[out.i] = tile;
+        mbar_arrive(smem_u32(&tile_full[out.i]));
+        out.next();
       }
       // the answers to the requests that were still open when none was left
-      for (int i = 1; i < kGwAhead && ok; ++i) {
-        ok = mbar_wait_cluster(smem_u32(&next_full[nx.slot]), nx.phase, abort_flag, err, kErrWaitDrain);
-        if (++nx.slot == kGwSlots) { nx.slot = 0; nx.phase ^= 1u; }
-      }
+      for (int i = 1; i < kGwAhead && ok; ++i) answer();
       if (!ok) {   // gave up: let the copies in flight land before the CTA's memory is handed on
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
       } else {   // every stage released: no copy of this CTA is in flight
-        for (int s = 0; s < kGemmStages; ++s) {
+        for (int s = 0; s < kGwStages; ++s) {
           if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, err, kErrWaitDrain)) break;
-          if (++stage == kGemmStages) { stage = 0; phase ^= 1u; }
+          if (++stage == kGwStages) { stage = 0; phase ^= 1u; }
         }
       }
     }
@@ -269,7 +295,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
-      Next nx;
+      Slot sl;
       for (int tile = first; tile >= 0 && ok;) {
         const GpTile c = tile_of(tile);
         const uint32_t idesc = idesc_bf16_f32(kPairBM, tile_cols(c.n)) | kIdescAMn | kIdescBMn;
@@ -284,18 +310,18 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             ok = mbar_wait(smem_u32(&full[stage]), phase, abort_flag, err, kErrWaitMma);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t sa = smem_u32(base + (size_t)stage * kGemmStageBytes);
-            const uint64_t ad = sdesc_mn_sw128(sa), bd = sdesc_mn_sw128(sa + kGemmBOff);
-            const int steps = kb == c.kb - 1 ? (tail_rows(c) + 15) >> 4 : kGpBoxRows / 16;
+            const uint32_t sa = smem_u32(base + (size_t)stage * kGwStageBytes);
+            const uint64_t ad = sdesc_mn_sw128(sa, kGwBox), bd = sdesc_mn_sw128(sa + 2 * kGwBox, kGwBox);
+            const int steps = kb == c.kb - 1 ? (tail_rows(c) + 15) >> 4 : kGwRows / 16;
 #pragma unroll
-            for (int k = 0; k < kGpBoxRows / 16; ++k)   // 16 rows of 128 bytes a step
+            for (int k = 0; k < kGwRows / 16; ++k)   // 16 rows of 128 bytes a step
               if (k < steps) tc_mma_f16_pair(dt, ad + 128u * k, bd + 128u * k, idesc, (kb != kc) | k);
             tc_commit_pair_mc(smem_u32(&empty[stage]), 0x3);
-            if (++stage == kGemmStages) { stage = 0; phase ^= 1u; }
+            if (++stage == kGwStages) { stage = 0; phase ^= 1u; }
           }
           if (ok) tc_commit_pair_mc(smem_u32(&acc_full[acc]), 0x3);
         }
-        if (ok) tile = next_tile(nx);
+        if (ok) tile = next_tile(sl);
       }
       tc_commit_pair_mc(smem_u32(drain), 0x3);
     }
@@ -304,11 +330,11 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     // ------------------------------------------------------------------ zeroing of tail rows
     int stage = 0;
     uint32_t tail_phase = 0;   // a bit per stage
-    Next nx;
+    Slot sl;
     for (int tile = first; tile >= 0;) {
       const GpTile c = tile_of(tile);
-      const int last = (stage + c.kb + kGemmStages - 1) % kGemmStages;
-      stage = (stage + c.kb) % kGemmStages;
+      const int last = (stage + c.kb + kGwStages - 1) % kGwStages;
+      stage = (stage + c.kb) % kGwStages;
       const int t = tail_rows(c);
       if (c.kb > 0 && (t & 15) != 0) {
         int ok = 1;
@@ -317,10 +343,10 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         __syncwarp();
         // rows [t, 16 ceil(t / 16)) of the stage's four boxes, 128 bytes a row (the swizzle
         // permutes 16-byte chunks within a row)
-        uint8_t* sp = base + (size_t)last * kGemmStageBytes;
+        uint8_t* sp = base + (size_t)last * kGwStageBytes;
         const int nz = ((t + 15) & ~15) - t;
         for (int i = lane; i < nz * 32; i += 32)
-          *reinterpret_cast<uint4*>(sp + ((i >> 3) & 3) * kGpBox + (t + (i >> 5)) * 128 + (i & 7) * 16) =
+          *reinterpret_cast<uint4*>(sp + ((i >> 3) & 3) * kGwBox + (t + (i >> 5)) * 128 + (i & 7) * 16) =
               make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_shared();   // the zeros, before the tensor cores read the stage
         __syncwarp();
@@ -335,7 +361,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
         tail_phase ^= 1u << last;
       }
-      if (lane == 0) tile = next_tile(nx);
+      if (lane == 0) tile = next_tile(sl);
       tile = __shfl_sync(0xffffffffu, tile, 0);
     }
   } else {
@@ -344,7 +370,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     const int half = (warp - 2) >> 2;       // which half of the tile's columns
     uint8_t* stage_out = store_base + (warp - 2) * kGwStoreBytes;
     int it = 0;
-    Next nx;
+    Slot sl;
     for (int tile = first; tile >= 0;) {
       const GpTile c = tile_of(tile);
       // this thread's row of 128 columns; an expert without rows leaves zeros
@@ -393,12 +419,11 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
           if (col0 + x * kGwStoreCols >= a.K) break;
           if (lane == 0) bulk_wait_read();
           __syncwarp();
-          // 16-byte chunk i of this row's 64 bytes at i ^ (row / 2 % 4)
-          const uint32_t* v = &s[x >> 1][(x & 1) * kGwStoreCols];
+          // 16-byte chunk i of this row's 128 bytes at i ^ (row % 8)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(stage_out + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(stage_out + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                make_uint4(s[x][4 * i], s[x][4 * i + 1], s[x][4 * i + 2], s[x][4 * i + 3]);
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {
@@ -407,8 +432,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) tile = next_tile(nx);
+      if (lane == 0) tile = next_tile(sl);
       tile = __shfl_sync(0xffffffffu, tile, 0);
     }
     if (lane == 0) bulk_wait_all();

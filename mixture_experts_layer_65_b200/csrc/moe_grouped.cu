@@ -64,8 +64,8 @@ moe_status pair_clusters(const void* kernel, int threads, size_t smem, std::atom
   return MOE_OK;
 }
 
-// fp32 [depth, outer, inner], boxes of 32 rows x 16 values (64 bytes, 64-byte swizzle): the
-// weight gradients' stores.
+// fp32 [depth, outer, inner], boxes of 32 rows x 32 values (128-byte swizzle): the weight
+// gradients' stores.
 bool encode_out_f32(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t depth) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return false;
@@ -74,7 +74,7 @@ bool encode_out_f32(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t ou
   cuuint32_t box[3] = {kGwStoreCols, 32, 1};
   cuuint32_t ess[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(ptr), dims, strides, box, ess,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -85,7 +85,7 @@ moe_status launch_tc(const void* a, const void* b, const int32_t* counts, const 
   static std::atomic<int> kept[64];
   constexpr bool W = OP == kGroupedWgrad;
   CUtensorMap tmA, tmB;
-  const bool ok = W ? encode_2d(&tmA, a, s.n, s.rows, kGpBoxRows) && encode_2d(&tmB, b, s.k, s.rows, kGpBoxRows)
+  const bool ok = W ? encode_2d(&tmA, a, s.n, s.rows, kGwRows) && encode_2d(&tmB, b, s.k, s.rows, kGwRows)
                     : encode_2d(&tmA, a, OP == kGroupedMM ? s.k : s.n, s.rows, 128) &&
                           encode_3d(&tmB, b, s.k, s.n, s.G, 128);
   if (!ok) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for a grouped product's operand");
