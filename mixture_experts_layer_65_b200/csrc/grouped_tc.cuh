@@ -75,6 +75,16 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
   }
 }
 
+// Arrive on a barrier that hands no memory over (a tensor-memory accumulator that has been
+// read into registers, a slot whose value has been used).  A releasing arrive would first wait
+// for the thread's earlier global stores.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -275,7 +285,7 @@ grouped_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[acc]), 0));
+      if (lane == 0) mbar_arrive_relaxed_cluster(mapa_shared(smem_u32(&acc_empty[acc]), 0));
       if (!row_ok) continue;
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + orow * out_cols + col0;
       const int left = out_cols - col0;   // a multiple of 8

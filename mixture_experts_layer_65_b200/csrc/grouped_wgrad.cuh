@@ -22,14 +22,15 @@
 // Balance: a tile's time goes with its expert's rows, which may differ a hundredfold.  The
 // grid has one cluster per tile, experts with most rows first; a running cluster takes the
 // next unstarted one over (clusterlaunchcontrol), so no cluster is left with a long tile at
-// the end, and which cluster computes a tile does not change its value.  The leader's producer
-// asks, both CTAs' producers read the answer and hand the tile on to their CTA's warps.
+// the end, and which cluster computes a tile does not change its value.  A warp of each CTA does
+// nothing but ask (the leader's), read the answer and hand the tile on: in the producer that
+// took 2,400 cycles a tile, which the ring could not cover.
 //
-// Output: each epilogue warp passes its 32 rows through shared memory, 32 columns at a
-// time (128-byte swizzled rows; with rows of 64 bytes the TMA unit's requests bounded the
-// kernel: 141 us instead of XX for 738 MB of zeros), to TMA stores, which cut off what lies outside dW; an
-// accumulating call makes them reductions (one addition per element, rounded to nearest;
-// subnormal sums become 0), so nothing is read back.
+// Output: each epilogue warp passes its 32 rows through shared memory, 32 columns (a box of
+// 128-byte swizzled rows) at a time, to TMA stores, which cut off what lies outside dW.  Plain
+// stores want registers that the sums of a 128-column row leave none of (738 MB of zeros: 255 us
+// against 119); an accumulating call makes them reductions (one addition per element, rounded
+// to nearest; subnormal sums become 0), so nothing is read back.
 #pragma once
 
 #include "grouped_tc.cuh"
@@ -37,13 +38,13 @@
 namespace moe {
 
 // A stage: 112 rows (seven MMA steps), two boxes of 64 columns each of dy and x; what is left of
-// the shared memory beside three of them holds the stores' staging.
+// the shared memory beside three of them holds the output's staging.
 constexpr int kGwRows = 112;
 constexpr int kGwStages = 3;
 constexpr uint32_t kGwBox = kGwRows * 128;
 constexpr uint32_t kGwStageBytes = 4 * kGwBox;
 constexpr int kGwChunk = 4;                                // stages per accumulator chain
-constexpr int kGwThreads = 64 + 32 * (kGpEpiWarps + 1);    // + the zeroing warp
+constexpr int kGwThreads = 64 + 32 * (kGpEpiWarps + 2);    // + the zeroing and the scheduling warp
 constexpr int kGwSlots = 4;                                // answers, and tiles handed on
 constexpr int kGwAhead = 2;                                // requests made ahead
 constexpr int kGwStoreCols = 32;
@@ -156,8 +157,8 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
       mbar_init(smem_u32(&next_full[s]), 1);
       mbar_init(smem_u32(&next_empty[s]), 1);
       mbar_init(smem_u32(&tile_full[s]), 1);
-      // the zeroing warp, the epilogue warps and, in the leader, the MMA issuer
-      mbar_init(smem_u32(&tile_empty[s]), 1 + kGpEpiWarps + (leader ? 1 : 0));
+      // the producer, the zeroing warp, the epilogue warps and, in the leader, the MMA issuer
+      mbar_init(smem_u32(&tile_empty[s]), 2 + kGpEpiWarps + (leader ? 1 : 0));
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
@@ -212,11 +213,11 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
       if (++i == kGwSlots) { i = 0; phase ^= 1u; }
     }
   };
-  // The tile the producer hands on (one thread of each reader); -1: none left, or a wait ran out.
+  // The tile the scheduling warp hands on (one thread of each reader); -1: none left, or a wait ran out.
   auto next_tile = [&](Slot& sl) {
     if (!mbar_wait(smem_u32(&tile_full[sl.i]), sl.phase, abort_flag, err, kErrWaitProducer)) return -1;
     const int tile = tiles[sl.i];
-    mbar_arrive(smem_u32(&tile_empty[sl.i]));
+    if (tile >= -1) mbar_arrive_relaxed(smem_u32(&tile_empty[sl.i]));   // (always: the value has arrived)
     sl.next();
     return tile;
   };
@@ -228,25 +229,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      Slot ask, got, out;
-      auto request = [&] {   // (leader) ask for one more tile
-        ok = mbar_wait_cluster(smem_u32(&next_empty[ask.i]), ask.phase ^ 1u, abort_flag, err, kErrWaitProducer);
-        if (!ok) return;
-        mbar_arrive_expect_tx(smem_u32(&next_full[ask.i]), 16);
-        mbar_arrive_expect_tx_peer(mapa_shared(smem_u32(&next_full[ask.i]), 1), 16);
-        clc_try_cancel(smem_u32(answers[ask.i]), smem_u32(&next_full[ask.i]));
-        ask.next();
-      };
-      auto answer = [&] {   // the next answer: a tile or -1
-        ok = mbar_wait_cluster(smem_u32(&next_full[got.i]), got.phase, abort_flag, err, kErrWaitProducer);
-        if (!ok) return -1;
-        const int cta = clc_answer(smem_u32(answers[got.i]));
-        fence_proxy_async_shared();   // read before the next answer is written
-        if (!leader) mbar_arrive_cluster(mapa_shared(smem_u32(&next_empty[got.i]), 0));
-        got.next();
-        return cta < 0 ? -1 : cta >> 1;
-      };
-      for (int i = 0; i < kGwAhead && leader && ok; ++i) request();
+      Slot sl;
       for (int tile = first; tile >= 0 && ok;) {
         const GpTile c = tile_of(tile);
         const int a0 = c.m * kPairBM + (int)rank * 128;
@@ -267,18 +250,8 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
           tma_load_2d_pair(sa + 2 * kGwBox + kGwBox, &tmB, fb, b0 + 64, row);
           if (++stage == kGwStages) { stage = 0; phase ^= 1u; }
         }
-        if (!ok) break;
-        tile = answer();
-        if (tile >= 0 && leader) request();
-        if (!ok) break;
-        ok = mbar_wait(smem_u32(&tile_empty[out.i]), out.phase ^ 1u, abort_flag, err, kErrWaitProducer);
-        if (!ok) break;
-        tiles[out.i] = tile;
-        mbar_arrive(smem_u32(&tile_full[out.i]));
-        out.next();
+        if (ok) tile = next_tile(sl);
       }
-      // the answers to the requests that were still open when none was left
-      for (int i = 1; i < kGwAhead && ok; ++i) answer();
       if (!ok) {   // gave up: let the copies in flight land before the CTA's memory is handed on
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
@@ -364,6 +337,47 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
       if (lane == 0) tile = next_tile(sl);
       tile = __shfl_sync(0xffffffffu, tile, 0);
     }
+  } else if (warp == 3 + kGpEpiWarps) {
+    // ------------------------------------------------------------------ tiles to take over
+    if (lane == 0) {
+      bool ok = true;
+      Slot ask, got, out;
+      auto request = [&] {   // (leader) ask for one more tile
+        ok = mbar_wait_cluster(smem_u32(&next_empty[ask.i]), ask.phase ^ 1u, abort_flag, err, kErrWaitProducer);
+        if (!ok) return;
+        mbar_arrive_expect_tx(smem_u32(&next_full[ask.i]), 16);
+        mbar_arrive_expect_tx_peer(mapa_shared(smem_u32(&next_full[ask.i]), 1), 16);
+        clc_try_cancel(smem_u32(answers[ask.i]), smem_u32(&next_full[ask.i]));
+        ask.next();
+      };
+      auto answer = [&] {   // the next answer: a tile or -1
+        ok = mbar_wait_cluster(smem_u32(&next_full[got.i]), got.phase, abort_flag, err, kErrWaitProducer);
+        if (!ok) return -1;
+        const int cta = clc_answer(smem_u32(answers[got.i]));
+        fence_proxy_async_shared();   // read before the next answer is written
+        if (!leader) mbar_arrive_cluster(mapa_shared(smem_u32(&next_empty[got.i]), 0));
+        got.next();
+        return cta < 0 ? -1 : cta >> 1;
+      };
+      for (int i = 0; i < kGwAhead && leader && ok; ++i) request();
+      for (int tile = first; tile >= 0;) {
+        tile = answer();
+        if (ok && tile >= 0 && leader) request();
+        if (!ok) break;
+        ok = mbar_wait(smem_u32(&tile_empty[out.i]), out.phase ^ 1u, abort_flag, err, kErrWaitProducer);
+        if (!ok) break;
+        tiles[out.i] = tile;
+        mbar_arrive(smem_u32(&tile_full[out.i]));
+        out.next();
+      }
+      // the answers to the requests that were still open when none was left
+      for (int i = 1; i < kGwAhead && ok; ++i) answer();
+      if (!ok) {   // gave up: let the answers in flight land
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+      }
+    }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------------ epilogue
     const int q = warp & 3;                 // TMEM lane quadrant
@@ -408,7 +422,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[acc]), 0));
+        if (lane == 0) mbar_arrive_relaxed_cluster(mapa_shared(smem_u32(&acc_empty[acc]), 0));
       }
       if (!ok) break;
       const int mrow0 = c.m * kPairBM + (int)rank * 128 + q * 32;   // first of this warp's rows
