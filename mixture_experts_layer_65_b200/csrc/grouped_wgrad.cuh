@@ -52,6 +52,12 @@ constexpr uint32_t kGwStoreBytes = 32 * kGwStoreCols * 4;  // one epilogue warp'
 constexpr size_t kGwSmemBytes = 1024 + kGwStages * kGwStageBytes + 1024 + kGpEpiWarps * kGwStoreBytes;
 static_assert(kGwBox % 1024 == 0 && kGwRows % 16 == 0, "swizzle atoms, MMA steps");
 
+struct GroupedWgradArgs {
+  const int32_t* counts;
+  int G, rows, N, K;     // dW is [G, N, K]
+  int accumulate;        // add to dW
+};
+
 // The experts' first rows, and the experts in order of falling row counts.
 struct WgradTable {
   int32_t row0[kGroupedMaxGroups + 1];
@@ -113,7 +119,7 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 
 static __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGwThreads, 1)
 grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ CUtensorMap tmOut, GroupedPairArgs a) {
+                     const __grid_constant__ CUtensorMap tmOut, GroupedWgradArgs a) {
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   __shared__ WgradTable tab;
@@ -190,22 +196,27 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   }
   __syncthreads();
 
+  struct Tile {
+    int g, m, n;      // expert, 256-row block, 256-column block of dW_g
+    int row0, grows;  // the expert's rows
+    int kb;           // stages
+  };
   auto tile_of = [&](int tile) {
-    GpTile c;
+    Tile c;
     const int o = tile / per_group, local = tile - o * per_group;
     c.g = tab.order[o];
     c.m = local / nt;
     c.n = local - c.m * nt;
     c.row0 = tab.row0[c.g];
     c.grows = tab.row0[c.g + 1] - c.row0;
-    c.kb = (c.grows + kGwRows - 1) / kGwRows;   // stages
+    c.kb = (c.grows + kGwRows - 1) / kGwRows;
     return c;
   };
   auto tile_cols = [&](int n) {   // the MMA's N: a multiple of 32
     const int left = a.K - n * kGemmBN;
     return left >= kGemmBN ? kGemmBN : (left + 31) & ~31;
   };
-  auto tail_rows = [&](const GpTile& c) { return c.grows - (c.kb - 1) * kGwRows; };   // of the last stage
+  auto tail_rows = [&](const Tile& c) { return c.grows - (c.kb - 1) * kGwRows; };   // of the last stage
   struct Slot {
     int i = 0;
     uint32_t phase = 0;
@@ -231,7 +242,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
       bool ok = true;
       Slot sl;
       for (int tile = first; tile >= 0 && ok;) {
-        const GpTile c = tile_of(tile);
+        const Tile c = tile_of(tile);
         const int a0 = c.m * kPairBM + (int)rank * 128;
         const int b0 = c.n * kGemmBN + (int)rank * (tile_cols(c.n) / 2);
         for (int kb = 0; kb < c.kb; ++kb) {
@@ -270,7 +281,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
       bool ok = true;
       Slot sl;
       for (int tile = first; tile >= 0 && ok;) {
-        const GpTile c = tile_of(tile);
+        const Tile c = tile_of(tile);
         const uint32_t idesc = idesc_bf16_f32(kPairBM, tile_cols(c.n)) | kIdescAMn | kIdescBMn;
         for (int kc = 0; kc < c.kb && ok; kc += kGwChunk, ++it) {
           const int kend = c.kb - kc < kGwChunk ? c.kb : kc + kGwChunk;
@@ -305,7 +316,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     uint32_t tail_phase = 0;   // a bit per stage
     Slot sl;
     for (int tile = first; tile >= 0;) {
-      const GpTile c = tile_of(tile);
+      const Tile c = tile_of(tile);
       const int last = (stage + c.kb + kGwStages - 1) % kGwStages;
       stage = (stage + c.kb) % kGwStages;
       const int t = tail_rows(c);
@@ -386,7 +397,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     int it = 0;
     Slot sl;
     for (int tile = first; tile >= 0;) {
-      const GpTile c = tile_of(tile);
+      const Tile c = tile_of(tile);
       // this thread's row of 128 columns; an expert without rows leaves zeros
       uint32_t s[4][32];
       if (c.kb == 0) {

@@ -2,7 +2,7 @@
 // (include/moe.h): checks, the choice of kernel, TMA descriptors and the launch.
 #include "op_common.cuh"
 #include "grouped_mm.cuh"
-#include "grouped_tc.cuh"
+#include "grouped_rows.cuh"
 #include "grouped_wgrad.cuh"
 
 using namespace moe;
@@ -83,30 +83,32 @@ template <int OP>
 moe_status launch_tc(const void* a, const void* b, const int32_t* counts, const Shape& s, int accumulate,
                      void* out, int device, int n_sms, cudaStream_t st) {
   static std::atomic<int> kept[64];
-  constexpr bool W = OP == kGroupedWgrad;
   CUtensorMap tmA, tmB;
-  const bool ok = W ? encode_2d(&tmA, a, s.n, s.rows, kGwRows) && encode_2d(&tmB, b, s.k, s.rows, kGwRows)
-                    : encode_2d(&tmA, a, OP == kGroupedMM ? s.k : s.n, s.rows, 128) &&
-                          encode_3d(&tmB, b, s.k, s.n, s.G, 128);
-  if (!ok) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for a grouped product's operand");
-  const int out_cols = OP == kGroupedMM ? s.n : s.k;
-  const int64_t nt = (out_cols + kGemmBN - 1) / kGemmBN;
-  GroupedPairArgs p{counts, s.G, (int)s.rows, s.n, s.k, out, accumulate,
-                    !misaligned(out, 32) && (out_cols * (W ? 4 : 2)) % 32 == 0};
   int clusters = 0;
-  if constexpr (W) {
+  if constexpr (OP == kGroupedWgrad) {
     CUtensorMap tmOut;
-    if (!encode_out_f32(&tmOut, out, s.k, s.n, s.G))
-      return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the weight gradients");
+    if (!encode_2d(&tmA, a, s.n, s.rows, kGwRows) || !encode_2d(&tmB, b, s.k, s.rows, kGwRows) ||
+        !encode_out_f32(&tmOut, out, s.k, s.n, s.G))
+      return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for a grouped product's operand");
     MOE_TRY(pair_clusters((const void*)grouped_wgrad_kernel, kGwThreads, kGwSmemBytes, kept, device, n_sms, &clusters));
-    const int64_t tiles = s.G * nt * ((s.n + kPairBM - 1) / kPairBM);   // a cluster each
+    // a cluster per tile
+    const int64_t tiles = (int64_t)s.G * ((s.n + kPairBM - 1) / kPairBM) * ((s.k + kGemmBN - 1) / kGemmBN);
+    GroupedWgradArgs p{counts, s.G, (int)s.rows, s.n, s.k, accumulate};
     MOE_CUDA(launch_pdl(grouped_wgrad_kernel, dim3(2 * (unsigned)tiles), dim3(kGwThreads), kGwSmemBytes, st, tmA,
                         tmB, tmOut, p));
   } else {
-    MOE_TRY(pair_clusters((const void*)grouped_pair_kernel<OP>, kGpThreads, kGemmSmemBytes, kept, device, n_sms, &clusters));
-    const int64_t tiles = ((s.rows + kPairBM - 1) / kPairBM + (s.G < s.rows ? s.G : s.rows)) * nt;
-    MOE_CUDA(launch_pdl(grouped_pair_kernel<OP>, dim3(2 * (unsigned)(tiles < clusters ? tiles : clusters)),
-                        dim3(kGpThreads), kGemmSmemBytes, st, tmA, tmB, p));
+    const int rt = gr_tile_rows(s.rows, s.G);
+    if (!encode_2d(&tmA, a, OP == kGroupedMM ? s.k : s.n, s.rows, rt / 2) ||
+        !encode_3d(&tmB, b, s.k, s.n, s.G, OP == kGroupedMM ? 128 : kGemmKPS * kGemmBK))
+      return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for a grouped product's operand");
+    MOE_TRY(pair_clusters((const void*)grouped_rows_kernel<OP>, kGpThreads, kGrSmemBytes, kept, device, n_sms,
+                          &clusters));
+    // at most: every expert with rows has one ragged tile row
+    const int64_t tiles = ((s.rows + rt - 1) / rt + (s.G < s.rows ? s.G : s.rows)) *
+                          (((OP == kGroupedMM ? s.n : s.k) + kPairBM - 1) / kPairBM);
+    GroupedRowsArgs p{counts, s.G, (int)s.rows, s.n, s.k, static_cast<__nv_bfloat16*>(out), rt};
+    MOE_CUDA(launch_pdl(grouped_rows_kernel<OP>, dim3(2 * (unsigned)(tiles < clusters ? tiles : clusters)),
+                        dim3(kGpThreads), kGrSmemBytes, st, tmB, tmA, p));
   }
   return MOE_OK;
 }
