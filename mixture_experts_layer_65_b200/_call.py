@@ -13,7 +13,7 @@ def check_tensor(name: str, t, device, shape: tuple, dtype) -> None:
     """`t` must be a contiguous CUDA tensor on `device` of the given shape and dtype."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
 
 
@@ -38,10 +38,11 @@ class on_stream:
 
     def __enter__(self) -> int:
         if self.stream is None:
+            current = torch.cuda.current_stream(self.device)
             if torch.cuda.current_device() != self.device.index:
                 self.ctx = torch.cuda.device(self.device)
                 self.ctx.__enter__()
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return current.cuda_stream
         if self.stream.device != self.device:
             raise ValueError(f"stream is on {self.stream.device}, the tensors are on {self.device}")
         if self.stream != torch.cuda.current_stream(self.device):

@@ -101,9 +101,10 @@ __device__ __forceinline__ int group_of(const GroupTable& t, int G, int tile) {
 }
 
 // ------------------------------------------------------------------------ CUDA cores
-// fp32 operands, and bf16 ones whose widths or addresses TMA cannot take: 64 x 64 tiles,
-// 16-deep steps, 4 x 4 outputs a thread, fp32 FMA.
-constexpr int kGsBM = 64, kGsBN = 64, kGsBK = 16, kGsThreads = 256;
+// fp32 operands, and bf16 ones whose widths or addresses TMA cannot take: fp32 FMA on
+// BM x BN tiles, a thread R x R outputs, 16-deep steps through two buffers in shared memory (the
+// next step's elements are on their way in registers while this one is computed).
+constexpr int kGsBK = 16;
 
 struct GroupedSimtArgs {
   const void* a;        // mm: x, dgrad: dy, wgrad: dy
@@ -124,79 +125,109 @@ __device__ __forceinline__ float to_f32(T v) {
 //   mm:    A[m, q] = x[row0 + m][q]       B[n, q] = W[n][q]      q < K
 //   dgrad: A[m, q] = dy[row0 + m][q]      B[n, q] = W[q][n]      q < N
 //   wgrad: A[m, q] = dy[row0 + q][m]      B[n, q] = x[row0 + q][n]   q < rows of the group
-template <typename T, int OP>
-__global__ void __launch_bounds__(kGsThreads) grouped_simt_kernel(GroupedSimtArgs p) {
+template <typename T, int OP, int BM, int BN, int R>
+__global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(GroupedSimtArgs p) {
+  constexpr int kThreads = BM * BN / (R * R);
+  constexpr int kA = BM * kGsBK / kThreads, kB = BN * kGsBK / kThreads;   // elements a thread loads
+  constexpr bool W = OP == kGroupedWgrad;
   pdl_launch_dependents();
   pdl_wait();
   __shared__ GroupTable tab;
-  __shared__ float As[kGsBK][kGsBM + 4];
-  __shared__ float Bs[kGsBK][kGsBN + 4];
-  constexpr bool W = OP == kGroupedWgrad;
+  __shared__ __align__(16) float As[2][kGsBK][BM + 4];
+  __shared__ __align__(16) float Bs[2][kGsBK][BN + 4];
   const int out_cols = OP == kGroupedMM ? p.N : p.K;
-  const int nt = (out_cols + kGsBN - 1) / kGsBN;
-  const int mt_w = (p.N + kGsBM - 1) / kGsBM;   // row tiles of a weight gradient
-  group_table(tab, p.counts, p.G, p.rows, W ? 0 : kGsBM, W ? nt * mt_w : nt);
+  const int nt = (out_cols + BN - 1) / BN;
+  const int mt_w = (p.N + BM - 1) / BM;   // row tiles of a weight gradient
+  group_table(tab, p.counts, p.G, p.rows, W ? 0 : BM, W ? nt * mt_w : nt);
   const int total = tab.tile0[p.G];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int tid = threadIdx.x, tx = tid % (BN / R), ty = tid / (BN / R);
+  const int lda = OP == kGroupedMM ? p.K : p.N;
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
     const int g = group_of(tab, p.G, tile);
     const int local = tile - tab.tile0[g];
-    const int m0 = local / nt * kGsBM, n0 = (local - local / nt * nt) * kGsBN;
+    const int m0 = local / nt * BM, n0 = (local - local / nt * nt) * BN;
     const int grow0 = tab.row0[g], grows = tab.row0[g + 1] - grow0;
     const int M = W ? p.N : grows;
     const int Q = OP == kGroupedMM ? p.K : OP == kGroupedDgrad ? p.N : grows;
-    const T* A = static_cast<const T*>(p.a) + (size_t)grow0 * (OP == kGroupedMM ? p.K : p.N);
+    const T* A = static_cast<const T*>(p.a) + (size_t)grow0 * lda;
     const T* B = static_cast<const T*>(p.b) + (W ? (size_t)grow0 * p.K : (size_t)g * p.N * p.K);
-    float acc[4][4];
+    T ra[kA], rb[kB];
+    // consecutive threads along each operand's contiguous index
+    auto fetch = [&](int q0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    for (int q0 = 0; q0 < Q; q0 += kGsBK) {
-#pragma unroll
-      for (int l = 0; l < kGsBM * kGsBK / kGsThreads; ++l) {
-        const int idx = tid + l * kGsThreads;
-        // consecutive threads along the operand's contiguous index
-        int m, q;
-        if constexpr (W) { m = idx % kGsBM; q = idx / kGsBM; }
-        else { q = idx % kGsBK; m = idx / kGsBK; }
-        float v = 0.f;
+      for (int l = 0; l < kA; ++l) {
+        const int idx = tid + l * kThreads;
+        const int m = W ? idx % BM : idx / kGsBK, q = W ? idx / BM : idx % kGsBK;
+        ra[l] = T(0.f);
         if (m0 + m < M && q0 + q < Q)
-          v = to_f32(W ? A[(size_t)(q0 + q) * p.N + m0 + m]
-                       : A[(size_t)(m0 + m) * (OP == kGroupedMM ? p.K : p.N) + q0 + q]);
-        As[q][m] = v;
-        int n, r;
-        if constexpr (OP == kGroupedMM) { r = idx % kGsBK; n = idx / kGsBK; }
-        else { n = idx % kGsBN; r = idx / kGsBN; }
-        v = 0.f;
-        if (n0 + n < out_cols && q0 + r < Q)
-          v = to_f32(OP == kGroupedMM ? B[(size_t)(n0 + n) * p.K + q0 + r] : B[(size_t)(q0 + r) * p.K + n0 + n]);
-        Bs[r][n] = v;
+          ra[l] = W ? A[(size_t)(q0 + q) * lda + m0 + m] : A[(size_t)(m0 + m) * lda + q0 + q];
       }
-      __syncthreads();
 #pragma unroll
-      for (int q = 0; q < kGsBK; ++q) {
-        float av[4], bv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) av[i] = As[q][ty * 4 + i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) bv[j] = Bs[q][tx * 4 + j];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+      for (int l = 0; l < kB; ++l) {
+        const int idx = tid + l * kThreads;
+        const int n = OP == kGroupedMM ? idx / kGsBK : idx % BN, q = OP == kGroupedMM ? idx % kGsBK : idx / BN;
+        rb[l] = T(0.f);
+        if (n0 + n < out_cols && q0 + q < Q)
+          rb[l] = OP == kGroupedMM ? B[(size_t)(n0 + n) * p.K + q0 + q] : B[(size_t)(q0 + q) * p.K + n0 + n];
       }
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+      for (int l = 0; l < kA; ++l) {
+        const int idx = tid + l * kThreads;
+        As[buf][W ? idx / BM : idx % kGsBK][W ? idx % BM : idx / kGsBK] = to_f32(ra[l]);
+      }
+#pragma unroll
+      for (int l = 0; l < kB; ++l) {
+        const int idx = tid + l * kThreads;
+        Bs[buf][OP == kGroupedMM ? idx % kGsBK : idx / BN][OP == kGroupedMM ? idx / kGsBK : idx % BN] = to_f32(rb[l]);
+      }
+    };
+    // a thread's outputs: R / 4 runs of four rows (columns), BM / (R / 4) (BN / (R / 4)) apart
+    float acc[R][R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < R; ++j) acc[i][j] = 0.f;
+    constexpr int kRunM = BM / (R / 4), kRunN = BN / (R / 4);
+    if (Q > 0) {
+      fetch(0);
+      __syncthreads();   // the previous tile's last step has been read
+      put(0);
       __syncthreads();
+      int buf = 0;
+      for (int q0 = 0; q0 < Q; q0 += kGsBK, buf ^= 1) {
+        const bool more = q0 + kGsBK < Q;
+        if (more) fetch(q0 + kGsBK);
+#pragma unroll
+        for (int q = 0; q < kGsBK; ++q) {
+          float av[R], bv[R];
+#pragma unroll
+          for (int i = 0; i < R; i += 4) {
+            *reinterpret_cast<float4*>(&av[i]) = *reinterpret_cast<const float4*>(&As[buf][q][i / 4 * kRunM + ty * 4]);
+            *reinterpret_cast<float4*>(&bv[i]) = *reinterpret_cast<const float4*>(&Bs[buf][q][i / 4 * kRunN + tx * 4]);
+          }
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < R; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+        }
+        if (more) {
+          put(buf ^ 1);
+          __syncthreads();
+        }
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = m0 + ty * 4 + i;
+    for (int i = 0; i < R; ++i) {
+      const int m = m0 + i / 4 * kRunM + ty * 4 + i % 4;
       if (m >= M) continue;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx * 4 + j;
+      for (int j = 0; j < R; ++j) {
+        const int n = n0 + j / 4 * kRunN + tx * 4 + j % 4;
         if (n >= out_cols) continue;
         if constexpr (W) {
+          if (Q == 0 && p.accumulate) continue;   // nothing to add: not touched
           float* o = static_cast<float*>(p.out) + ((size_t)g * p.N + m) * p.K + n;
           *o = p.accumulate ? *o + acc[i][j] : acc[i][j];
         } else {

@@ -1,5 +1,6 @@
 // moe_grouped.cu -- moe_grouped_mm, moe_grouped_mm_dgrad and moe_grouped_mm_wgrad
 // (include/moe.h): checks, the choice of kernel, TMA descriptors and the launch.
+#include <cstdlib>
 #include "op_common.cuh"
 #include "grouped_mm.cuh"
 #include "grouped_rows.cuh"
@@ -25,18 +26,36 @@ moe_status check_shape(const Shape& s) {
   if (s.rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows must not be negative");
   if (s.rows >= (int64_t(1) << 30)) return fail(MOE_ERR_UNSUPPORTED, "rows=%lld above 2^30", (long long)s.rows);
   // tiles of the smallest kind, all groups together, are counted in 32 bits
-  const int64_t nt = (s.n + 63) / 64, kt = (s.k + 63) / 64;
-  const int64_t mt = (s.rows + 63) / 64 + s.G;
+  const int64_t nt = (s.n + 31) / 32, kt = (s.k + 31) / 32;
+  const int64_t mt = (s.rows + 31) / 32 + s.G;
   if (mt * (nt > kt ? nt : kt) >= (int64_t(1) << 31) || nt * kt * s.G >= (int64_t(1) << 30))
     return fail(MOE_ERR_UNSUPPORTED, "too many tiles");
   return MOE_OK;
 }
 
+// The CUDA-core kernel with BM x BN tiles and R x R outputs a thread; its tiles at most.
+template <int OP>
+int64_t simt_tiles(const Shape& s, int bm, int bn) {
+  const int64_t nt = ((OP == kGroupedMM ? s.n : s.k) + bn - 1) / bn;
+  return OP == kGroupedWgrad ? s.G * nt * ((s.n + bm - 1) / bm)
+                             : ((s.rows + bm - 1) / bm + (s.G < s.rows ? s.G : s.rows)) * nt;
+}
+template <typename T, int OP, int BM, int BN, int R>
+cudaError_t launch_simt_tile(const GroupedSimtArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
+  constexpr int kThreads = BM * BN / (R * R);
+  const int64_t tiles = simt_tiles<OP>(s, BM, BN), most = (int64_t)n_sms * (1024 / kThreads);
+  return launch_pdl(grouped_simt_kernel<T, OP, BM, BN, R>, dim3((unsigned)(tiles < most ? tiles : most)),
+                    dim3(kThreads), 0, st, a);
+}
 template <typename T, int OP>
-cudaError_t launch_simt(const GroupedSimtArgs& a, int64_t tiles, int n_sms, cudaStream_t st) {
-  const int64_t most = (int64_t)n_sms * 6;
-  return launch_pdl(grouped_simt_kernel<T, OP>, dim3((unsigned)(tiles < most ? tiles : most)), dim3(kGsThreads), 0,
-                    st, a);
+cudaError_t launch_simt(const GroupedSimtArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
+  static const int force = getenv("MOE_SIMT") ? atoi(getenv("MOE_SIMT")) : 0;
+  if (force == 128) return launch_simt_tile<T, OP, 128, 128, 8>(a, s, n_sms, st);
+  if (force == 64) return launch_simt_tile<T, OP, 64, 64, 4>(a, s, n_sms, st);
+  if (force == 32) return launch_simt_tile<T, OP, 32, 32, 4>(a, s, n_sms, st);
+  if (simt_tiles<OP>(s, 128, 128) >= 2 * n_sms) return launch_simt_tile<T, OP, 128, 128, 8>(a, s, n_sms, st);
+  if (simt_tiles<OP>(s, 64, 64) >= n_sms) return launch_simt_tile<T, OP, 64, 64, 4>(a, s, n_sms, st);
+  return launch_simt_tile<T, OP, 32, 32, 4>(a, s, n_sms, st);
 }
 
 // Clusters of `kernel` that can be resident at once on the current device (asked for once per
@@ -137,13 +156,9 @@ moe_status product(const void* a, const void* b, const int32_t* counts, const Sh
   if (s.dtype == MOE_BF16 && s.n % 8 == 0 && s.k % 8 == 0 && s.rows > 0 && aligned16(a) && aligned16(b) &&
       aligned16(out))
     return launch_tc<OP>(a, b, counts, s, accumulate, out, device, n_sms, st);
-  const int out_cols = OP == kGroupedMM ? s.n : s.k;
   GroupedSimtArgs p{a, b, counts, out, s.G, (int)s.rows, s.n, s.k, accumulate};
-  const int64_t nt = (out_cols + kGsBN - 1) / kGsBN;
-  const int64_t tiles = W ? (int64_t)s.G * nt * ((s.n + kGsBM - 1) / kGsBM)
-                          : ((s.rows + kGsBM - 1) / kGsBM + (s.G < s.rows ? s.G : s.rows)) * nt;
-  MOE_CUDA((s.dtype == MOE_BF16 ? launch_simt<__nv_bfloat16, OP>(p, tiles, n_sms, st)
-                                : launch_simt<float, OP>(p, tiles, n_sms, st)));
+  MOE_CUDA((s.dtype == MOE_BF16 ? launch_simt<__nv_bfloat16, OP>(p, s, n_sms, st)
+                                : launch_simt<float, OP>(p, s, n_sms, st)));
   return MOE_OK;
 }
 

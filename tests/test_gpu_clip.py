@@ -161,8 +161,14 @@ def test_bindings_refuse():
         clip.clip_grad_norm([g, g.double()], 1.0)
     with pytest.raises(ValueError, match="outputs"):
         clip.clip_grad_norm([g], 1.0, out=[])
-    with pytest.raises(ValueError, match="shape"):
-        clip.clip_grad_norm([g], 1.0, out=[torch.zeros(64, device="cuda")])
+    with pytest.raises(ValueError, match="elements"):
+        clip.clip_grad_norm([g], 1.0, out=[torch.zeros(63, device="cuda")])
+    with pytest.raises(ValueError, match="type"):
+        clip.clip_grad_norm([g], 1.0, out=[torch.zeros(64, dtype=BF, device="cuda")])
+    with pytest.raises(ValueError, match=r"grads\[1\]"):
+        clip.clip_grad_norm([g, None], 1.0)
+    with pytest.raises(ValueError, match=r"out\[0\]"):
+        clip.clip_grad_norm([g], 1.0, out=[g.cpu()])
     with pytest.raises(RuntimeError, match="shares memory"):
         clip.clip_grad_norm([g, g], 1.0)
     with pytest.raises(RuntimeError, match="max_norm"):
