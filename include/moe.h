@@ -123,6 +123,13 @@ moe_status moe_forward(moe_handle* handle, const void* u, void* h, int32_t* topk
                        float* topk_w, int32_t* expert_counts, float* aux_loss,
                        moe_stream_t stream);
 
+/* moe_forward without the residual: y_t = sum_{j shared} FFN_j(u_t) + sum_{i in sel[t]} g[t,i]
+ * FFN_i(u_t), for a block whose residual stream is not the layer's input (moe_block_norm).
+ * Everything else as in moe_forward. */
+moe_status moe_forward_branch(moe_handle* handle, const void* u, void* y, int32_t* topk_idx,
+                              float* topk_w, int32_t* expert_counts, float* aux_loss,
+                              moe_stream_t stream);
+
 /* moe_forward on HOST buffers: copies u host->device, runs the forward, copies every
  * output device->host and synchronises `stream` before returning.  Sizes as in
  * moe_forward; any output pointer except h_host may be NULL (not copied back). */
@@ -199,6 +206,14 @@ moe_status moe_backward(moe_handle* handle, const void* u, const int32_t* topk_i
                         const float* topk_w, const int32_t* expert_counts, const void* dh,
                         float d_aux, void* du, float* d_centroids, float* d_bias,
                         float* d_w_gate, float* d_w_up, float* d_w_down, moe_stream_t stream);
+
+/* moe_backward after a moe_forward_branch (dy the gradient of its y): du has no residual
+ * term.  Either backward is refused after the other forward. */
+moe_status moe_backward_branch(moe_handle* handle, const void* u, const int32_t* topk_idx,
+                               const float* topk_w, const int32_t* expert_counts, const void* dy,
+                               float d_aux, void* du, float* d_centroids, float* d_bias,
+                               float* d_w_gate, float* d_w_up, float* d_w_down,
+                               moe_stream_t stream);
 
 /* Per-kernel timing.  After moe_timing_begin(handle, n), each of the next n calls of
  * moe_forward on this handle records a CUDA event on its stream before each of its

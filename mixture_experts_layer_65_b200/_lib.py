@@ -37,6 +37,7 @@ _P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 _SIGS = {
     "moe_create": (ctypes.c_int, [ctypes.POINTER(MoeCfg), ctypes.POINTER(ctypes.c_void_p)]),
     "moe_forward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_forward_branch": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P]),
     "moe_forward_host": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P]),
     "moe_forward_host_pipelined": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P]),
     "moe_pipeline_wait": (ctypes.c_int, [_P, _P]),
@@ -64,6 +65,8 @@ _SIGS = {
     "moe_backward_prepare": (ctypes.c_int, [_P]),
     "moe_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P,
                                     _P]),
+    "moe_backward_branch": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P,
+                                           _P, _P]),
     "moe_grouped_mm": (ctypes.c_int, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _P, _P]),
     "moe_grouped_mm_dgrad": (ctypes.c_int, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _P, _P]),
     "moe_grouped_mm_wgrad": (ctypes.c_int, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _I32, _P, _P]),

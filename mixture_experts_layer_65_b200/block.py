@@ -1,5 +1,6 @@
 """The norms before and after a block, fused with its gate, the residual scale and the
-residual add (moe_block_norm* in include/moe.h), forward and backward.
+residual add (moe_block_norm* in include/moe.h), forward and backward; and `MoEBlock`, a layer
+between them.
 
 Per row, s(v) = 1 / sqrt(mean(v^2) + eps):
   r = beta x + gate p,  p = y s(y) post_weight   (p = y without post_weight)
@@ -13,7 +14,8 @@ import torch
 
 from ._call import DTYPES, check_tensor, on_stream, rows_of
 from ._lib import check, lib
-from .layer import _ptr
+from .clip import clip_grad_norm
+from .layer import MoELayer, MoEOutput, _ptr
 
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 
@@ -124,3 +126,84 @@ def block_norm_backward(fwd: BlockNorm, y: torch.Tensor | None, *, dr: torch.Ten
             _ptr(g.dx), _ptr(g.dy), _ptr(g.d_gate), _ptr(g.d_post_weight), _ptr(g.d_pre_weight),
             _ptr(ws), size, s))
     return g
+
+
+class MoEBlockOutput(NamedTuple):
+    r: torch.Tensor              # [T, d] the residual stream after the block
+    norm_in: BlockNorm           # the norm before the layer: its u is the layer's input
+    layer: MoEOutput             # the layer without its residual
+    norm_out: BlockNorm          # r, and the next block's input when next_weight was given
+
+
+class MoEBlockGrads(NamedTuple):
+    dx: torch.Tensor                     # [T, d]; with norm_in given to forward: without its part
+    du: torch.Tensor | None              # that part: the gradient of norm_in.u (norm_in given)
+    d_gate: torch.Tensor | None
+    d_post_weight: torch.Tensor | None
+    d_pre_weight: torch.Tensor | None    # (None when norm_in was given)
+    d_next_weight: torch.Tensor | None
+    d_centroids: torch.Tensor
+    d_bias: torch.Tensor
+    d_w_gate: torch.Tensor | None
+    d_w_up: torch.Tensor | None
+    d_w_down: torch.Tensor | None
+    grad_norm: torch.Tensor | None       # [1] fp32, before clipping (max_norm given)
+
+    def parameters(self) -> list:
+        """The parameters' gradients that there are."""
+        return [t for t in self[2:11] if t is not None]
+
+
+class MoEBlock:
+    """r = beta x + gate * norm(FFN(norm(x))): a MoELayer (its experts without its own residual)
+    between the norms.  pre_weight [d], optional post_weight [d] and gate ([d], or [T, 1] given to
+    each call) are fp32.
+
+    In a stack, `next_weight` of one block's forward is the next block's pre_weight: the step
+    between two blocks is then one kernel, and its norm goes to the next forward as `norm_in`
+    (out.norm_out); the gradients go back the same way, dx and du of the later block as dr and du
+    of the earlier one's backward."""
+
+    def __init__(self, layer: MoELayer, pre_weight: torch.Tensor, post_weight: torch.Tensor | None = None,
+                 gate: torch.Tensor | None = None, beta: float = 1.0, eps: float = 1e-6):
+        self.layer, self.pre_weight, self.post_weight = layer, pre_weight, post_weight
+        self.gate, self.beta, self.eps = gate, beta, eps
+
+    def forward(self, x: torch.Tensor, *, gate: torch.Tensor | None = None, norm_in: BlockNorm | None = None,
+                next_weight: torch.Tensor | None = None,
+                stream: torch.cuda.Stream | None = None) -> MoEBlockOutput:
+        """`gate` replaces the block's own for this call; norm_in: the norm of x, computed by the
+        block before (its r is x)."""
+        if norm_in is None:
+            norm_in = block_norm(x, pre_weight=self.pre_weight, eps=self.eps, stream=stream)
+        elif norm_in.u is None:
+            raise ValueError("norm_in has no u: give the earlier block this block's pre_weight as next_weight")
+        with on_stream(x.device, stream):
+            out = self.layer.forward_branch(norm_in.u)
+        norm_out = block_norm(x, out.h, gate=self.gate if gate is None else gate, post_weight=self.post_weight,
+                              pre_weight=next_weight, beta=self.beta, eps=self.eps, stream=stream)
+        return MoEBlockOutput(norm_out.r, norm_in, out, norm_out)
+
+    __call__ = forward
+
+    def backward(self, out: MoEBlockOutput, dr: torch.Tensor | None, du: torch.Tensor | None = None, *,
+                 d_aux: float = 0.0, gate: torch.Tensor | None = None, norm_in_given: bool = False,
+                 next_weight: torch.Tensor | None = None, weights: bool = True,
+                 max_norm: float | None = None, stream: torch.cuda.Stream | None = None) -> MoEBlockGrads:
+        """Gradients of sum(dr r) + sum(du u_next) + d_aux aux after `forward` (the layer's last
+        one; the same gate, next_weight and whether norm_in was given).  max_norm: the parameters'
+        gradients are clipped to it together, and their norm before is returned."""
+        after = block_norm_backward(out.norm_out, out.layer.h, dr=dr, du=du,
+                                    gate=self.gate if gate is None else gate, post_weight=self.post_weight,
+                                    pre_weight=next_weight, beta=self.beta, stream=stream)
+        with on_stream(out.r.device, stream):
+            d_in, *rest = self.layer.backward_branch(out.norm_in.u, out.layer, after.dy, d_aux, weights)
+        dx, d_pre = after.dx, None
+        if not norm_in_given:
+            before = block_norm_backward(out.norm_in, None, dr=after.dx, du=d_in, pre_weight=self.pre_weight,
+                                         stream=stream)
+            dx, d_pre, d_in = before.dx, before.d_pre_weight, None
+        g = MoEBlockGrads(dx, d_in, after.d_gate, after.d_post_weight, d_pre, after.d_pre_weight, *rest, None)
+        if max_norm is not None:
+            g = g._replace(grad_norm=clip_grad_norm(g.parameters(), max_norm, stream=stream))
+        return g

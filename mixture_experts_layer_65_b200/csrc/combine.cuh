@@ -21,7 +21,7 @@ __host__ __device__ constexpr int combine_maxk(int top_k) {
 
 template <typename T>
 struct CombineArgs {
-  const T* u;              // [T, d]
+  const T* u;              // [T, d], or nullptr: no residual (moe_forward_branch)
   const T* ys;             // [>= T, d] shared-group output, or nullptr when K_s = 0
   const T* yr;             // [rows_cap, d] routed outputs (expert-contiguous rows)
   const int32_t* slot_row; // [T, top_k]
@@ -85,13 +85,13 @@ combine_bf16_kernel(CombineArgs<__nv_bfloat16> a) {
   }
   int v0, v1;
   combine_range(a.d >> 3, a.parts, gw - t * a.parts, v0, v1);
-  const uint4* ur = reinterpret_cast<const uint4*>(a.u + (size_t)t * a.d);
+  const uint4* ur = a.u ? reinterpret_cast<const uint4*>(a.u + (size_t)t * a.d) : nullptr;
   const uint4* sr = a.ys ? reinterpret_cast<const uint4*>(a.ys + (size_t)t * a.d) : nullptr;
   const uint4* xr = a.xtra ? reinterpret_cast<const uint4*>(a.xtra + (size_t)t * a.d) : nullptr;
   uint4* hr = reinterpret_cast<uint4*>(a.h + (size_t)t * a.d);
   for (int v = v0 + lane; v < v1; v += 32) {
     uint4 x[MAXK];
-    const uint4 xu = __ldg(ur + v);
+    const uint4 xu = ur ? __ldg(ur + v) : make_uint4(0u, 0u, 0u, 0u);
     const uint4 xs = sr ? __ldg(sr + v) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int k = 0; k < MAXK; ++k)
@@ -99,7 +99,7 @@ combine_bf16_kernel(CombineArgs<__nv_bfloat16> a) {
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    add8(acc, xu, 1.0f);
+    if (ur) add8(acc, xu, 1.0f);
     if (sr) add8(acc, xs, 1.0f);
 #pragma unroll
     for (int k = 0; k < MAXK; ++k)
@@ -131,11 +131,11 @@ static __global__ void __launch_bounds__(kCombineWarps * 32) combine_f32_kernel(
   __syncwarp();
   int v0, v1;
   combine_range(a.d >> 2, a.parts, gw - t * a.parts, v0, v1);
-  const float4* ur = reinterpret_cast<const float4*>(a.u + (size_t)t * a.d);
+  const float4* ur = a.u ? reinterpret_cast<const float4*>(a.u + (size_t)t * a.d) : nullptr;
   const float4* sr = a.ys ? reinterpret_cast<const float4*>(a.ys + (size_t)t * a.d) : nullptr;
   float4* hr = reinterpret_cast<float4*>(a.h + (size_t)t * a.d);
   for (int v = v0 + lane; v < v1; v += 32) {
-    float4 acc = __ldg(ur + v);
+    float4 acc = ur ? __ldg(ur + v) : make_float4(0.f, 0.f, 0.f, 0.f);
     if (sr) {
       const float4 s = __ldg(sr + v);
       acc.x += s.x; acc.y += s.y; acc.z += s.z; acc.w += s.w;

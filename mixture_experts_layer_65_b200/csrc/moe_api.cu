@@ -157,6 +157,7 @@ struct moe_handle {
   // backward's workspace
   bool bwd = false;
   bool bwd_forward = false;                // a forward ran since moe_backward_prepare
+  bool bwd_residual = true;                // and it added u to its output
   int kpad = 0;                            // n_pad rounded up to 64: K of the e-product GEMM
   float* logits = nullptr;                 // [T, n_routed]
   int32_t* ts3 = nullptr;                  // [G + 1] dHmid GEMM tiles (N = I at 256 per tile)
@@ -569,8 +570,10 @@ static inline void tick(moe_handle* H, cudaStream_t s, int slot) {
     cudaEventRecord(H->events[(size_t)H->timing_used * (kKernelsPerForward + 1) + slot], s);
 }
 
-moe_status moe_forward(moe_handle* H, const void* u, void* h, int32_t* topk_idx, float* topk_w,
-                       int32_t* expert_counts, float* aux_loss, moe_stream_t stream_) {
+// moe_forward (residual) and moe_forward_branch (without).
+static moe_status forward_impl(moe_handle* H, const void* u, void* h, int32_t* topk_idx, float* topk_w,
+                               int32_t* expert_counts, float* aux_loss, bool residual,
+                               moe_stream_t stream_) {
   if (!H) return fail(MOE_ERR_INVALID_ARG, "handle is NULL");
   if (!u || !h || !topk_idx || !topk_w || !expert_counts || !aux_loss)
     return fail(MOE_ERR_INVALID_ARG, "an input/output pointer is NULL");
@@ -772,7 +775,7 @@ moe_status moe_forward(moe_handle* H, const void* u, void* h, int32_t* topk_idx,
     MOE_CUDA(cudaGetLastError());
 
     const int parts = combine_parts(T, d / 4, H->n_sms);
-    CombineArgs<float> ca{static_cast<const float*>(u), static_cast<const float*>(H->ys),
+    CombineArgs<float> ca{residual ? static_cast<const float*>(u) : nullptr, static_cast<const float*>(H->ys),
                           static_cast<const float*>(H->yr), H->slot_row, topk_w,
                           static_cast<float*>(h), T, d, K, parts};
     tick(H, stream, 5);
@@ -782,7 +785,7 @@ moe_status moe_forward(moe_handle* H, const void* u, void* h, int32_t* topk_idx,
   }
   if (H->bf16) {
     const int parts = combine_parts(T, d / 8, H->n_sms);
-    CombineArgs<__nv_bfloat16> ca{static_cast<const __nv_bfloat16*>(u),
+    CombineArgs<__nv_bfloat16> ca{residual ? static_cast<const __nv_bfloat16*>(u) : nullptr,
                                   static_cast<const __nv_bfloat16*>(H->ys),
                                   static_cast<const __nv_bfloat16*>(H->yr), H->slot_row, topk_w,
                                   static_cast<__nv_bfloat16*>(h), T, d, K, parts};
@@ -798,8 +801,21 @@ moe_status moe_forward(moe_handle* H, const void* u, void* h, int32_t* topk_idx,
     tick(H, stream, kKernelsPerForward);
     ++H->timing_used;
   }
-  if (H->bwd) H->bwd_forward = true;
+  if (H->bwd) {
+    H->bwd_forward = true;
+    H->bwd_residual = residual;
+  }
   return MOE_OK;
+}
+
+moe_status moe_forward(moe_handle* H, const void* u, void* h, int32_t* topk_idx, float* topk_w,
+                       int32_t* expert_counts, float* aux_loss, moe_stream_t stream) {
+  return forward_impl(H, u, h, topk_idx, topk_w, expert_counts, aux_loss, true, stream);
+}
+
+moe_status moe_forward_branch(moe_handle* H, const void* u, void* y, int32_t* topk_idx, float* topk_w,
+                              int32_t* expert_counts, float* aux_loss, moe_stream_t stream) {
+  return forward_impl(H, u, y, topk_idx, topk_w, expert_counts, aux_loss, false, stream);
 }
 
 
@@ -932,13 +948,15 @@ moe_status moe_backward_prepare(moe_handle* H) {
   return MOE_OK;
 }
 
-moe_status moe_backward(moe_handle* H, const void* u, const int32_t* topk_idx, const float* topk_w,
-                        const int32_t* expert_counts, const void* dh, float d_aux, void* du,
-                        float* d_centroids, float* d_bias, float* d_w_gate, float* d_w_up,
-                        float* d_w_down, moe_stream_t stream_) {
+// moe_backward (residual: du includes dh) and moe_backward_branch.
+static moe_status backward_impl(moe_handle* H, const void* u, const int32_t* topk_idx, const float* topk_w,
+                                const int32_t* expert_counts, const void* dh, float d_aux, void* du,
+                                float* d_centroids, float* d_bias, float* d_w_gate, float* d_w_up,
+                                float* d_w_down, bool residual, moe_stream_t stream_) {
   if (!H) return fail(MOE_ERR_INVALID_ARG, "handle is NULL");
-  if (!H->bwd || !H->bwd_forward)
-    return fail(MOE_ERR_INVALID_ARG, "call moe_backward_prepare and then moe_forward first");
+  if (!H->bwd || !H->bwd_forward || H->bwd_residual != residual)
+    return fail(MOE_ERR_INVALID_ARG, "call moe_backward_prepare and then %s first",
+                residual ? "moe_forward" : "moe_forward_branch");
   if (!u || !topk_idx || !topk_w || !expert_counts || !dh || !du || !d_centroids)
     return fail(MOE_ERR_INVALID_ARG, "an input/output pointer is NULL");
   if (!aligned16(u) || !aligned16(dh) || !aligned16(du))
@@ -1028,7 +1046,7 @@ moe_status moe_backward(moe_handle* H, const void* u, const int32_t* topk_idx, c
   MOE_CUDA(cudaGetLastError());
   // 6. du = dh + dX_shared + sum_k dX_k + dl e (fixed order, one rounding)
   const int parts = combine_parts(T, d / 8, H->n_sms);
-  CombineArgs<__nv_bfloat16> ca{static_cast<const __nv_bfloat16*>(dh),
+  CombineArgs<__nv_bfloat16> ca{residual ? static_cast<const __nv_bfloat16*>(dh) : nullptr,
                                 H->has_shared ? static_cast<const __nv_bfloat16*>(H->dxs) : nullptr,
                                 static_cast<const __nv_bfloat16*>(H->dxr), H->slot_row, nullptr,
                                 static_cast<__nv_bfloat16*>(du), T, d, K, parts,
@@ -1118,6 +1136,22 @@ moe_status moe_backward(moe_handle* H, const void* u, const int32_t* topk_idx, c
              H->tmDhT, H->tmDyrT, H->tmHsT, H->tmHrT, w2);
   MOE_CUDA(cudaGetLastError());
   return MOE_OK;
+}
+
+moe_status moe_backward(moe_handle* H, const void* u, const int32_t* topk_idx, const float* topk_w,
+                        const int32_t* expert_counts, const void* dh, float d_aux, void* du,
+                        float* d_centroids, float* d_bias, float* d_w_gate, float* d_w_up,
+                        float* d_w_down, moe_stream_t stream) {
+  return backward_impl(H, u, topk_idx, topk_w, expert_counts, dh, d_aux, du, d_centroids, d_bias, d_w_gate,
+                       d_w_up, d_w_down, true, stream);
+}
+
+moe_status moe_backward_branch(moe_handle* H, const void* u, const int32_t* topk_idx, const float* topk_w,
+                               const int32_t* expert_counts, const void* dy, float d_aux, void* du,
+                               float* d_centroids, float* d_bias, float* d_w_gate, float* d_w_up,
+                               float* d_w_down, moe_stream_t stream) {
+  return backward_impl(H, u, topk_idx, topk_w, expert_counts, dy, d_aux, du, d_centroids, d_bias, d_w_gate,
+                       d_w_up, d_w_down, false, stream);
 }
 
 moe_status moe_timing_begin(moe_handle* H, int32_t max_forwards) {

@@ -130,15 +130,23 @@ class MoELayer:
     def forward(self, u: torch.Tensor, out: MoEOutput | None = None,
                 stream: torch.cuda.Stream | None = None) -> MoEOutput:
         """Enqueue one forward pass on `stream` (default: the current stream)."""
+        return self._forward(lib().moe_forward, u, out, stream)
+
+    def forward_branch(self, u: torch.Tensor, out: MoEOutput | None = None,
+                       stream: torch.cuda.Stream | None = None) -> MoEOutput:
+        """forward without the residual: `h` is the experts' part alone (for a block whose
+        residual stream is not the layer's input: block.MoEBlock)."""
+        return self._forward(lib().moe_forward_branch, u, out, stream)
+
+    def _forward(self, call, u, out, stream) -> MoEOutput:
         self._check_device_tensor("u", u, (self.T, self.d), self.torch_dtype)
         if out is None:
             out = self.alloc_outputs()
         else:
             self._check_outputs(out)
         s = stream or torch.cuda.current_stream(self.device)
-        check(lib().moe_forward(self._h, _ptr(u), _ptr(out.h), _ptr(out.topk_idx),
-                                _ptr(out.topk_w), _ptr(out.expert_counts), _ptr(out.aux_loss),
-                                s.cuda_stream))
+        check(call(self._h, _ptr(u), _ptr(out.h), _ptr(out.topk_idx), _ptr(out.topk_w),
+                   _ptr(out.expert_counts), _ptr(out.aux_loss), s.cuda_stream))
         return out
 
     __call__ = forward
@@ -207,6 +215,15 @@ class MoELayer:
         other forward in between): (du [T, d] bf16, d_centroids [n_routed, d] fp32,
         d_bias [n_routed] fp32, d_w_gate, d_w_up [G, inter, d] fp32, d_w_down [G, d, inter]
         fp32), G = n_shared + n_routed; the last three are None with weights=False."""
+        return self._backward(lib().moe_backward, u, out, dh, d_aux, weights, stream)
+
+    def backward_branch(self, u: torch.Tensor, out: MoEOutput, dy: torch.Tensor, d_aux: float = 0.0,
+                        weights: bool = True, stream: torch.cuda.Stream | None = None):
+        """backward after `forward_branch(u, out)`: dy is the gradient of its `h`, and du has no
+        residual term."""
+        return self._backward(lib().moe_backward_branch, u, out, dy, d_aux, weights, stream)
+
+    def _backward(self, call, u, out, dh, d_aux, weights, stream):
         self._check_device_tensor("u", u, (self.T, self.d), self.torch_dtype)
         self._check_device_tensor("dh", dh, (self.T, self.d), self.torch_dtype)
         self._check_outputs(out)
@@ -221,10 +238,9 @@ class MoELayer:
             dwu = torch.empty(G, self.inter, self.d, dtype=torch.float32, device=dev)
             dwd = torch.empty(G, self.d, self.inter, dtype=torch.float32, device=dev)
         s = stream or torch.cuda.current_stream(dev)
-        check(lib().moe_backward(self._h, _ptr(u), _ptr(out.topk_idx), _ptr(out.topk_w),
-                                 _ptr(out.expert_counts), _ptr(dh), float(d_aux), _ptr(du),
-                                 _ptr(d_cen), _ptr(d_bias), _ptr(dwg), _ptr(dwu), _ptr(dwd),
-                                 s.cuda_stream))
+        check(call(self._h, _ptr(u), _ptr(out.topk_idx), _ptr(out.topk_w), _ptr(out.expert_counts),
+                   _ptr(dh), float(d_aux), _ptr(du), _ptr(d_cen), _ptr(d_bias), _ptr(dwg), _ptr(dwu),
+                   _ptr(dwd), s.cuda_stream))
         return du, d_cen, d_bias, dwg, dwu, dwd
 
     DEBUG_BUFFERS = {"slot_row": 0, "xp": 1, "hr": 2, "yr": 3, "hs": 4, "ys": 5, "grp_row": 6,

@@ -53,3 +53,29 @@ def global_balance_loss(layer, out, psum_buf: torch.Tensor, counts_buf: torch.Te
     counts_buf.copy_(out.expert_counts)
     n_global = all_reduce_balance_stats(counts_buf, psum_buf, layer.T, group, n_global)
     return loss_fn(counts_buf, psum_buf, n_global, layer.alpha1, aux_buf)
+
+
+def clip_grad_norm(replicated, sharded, max_norm: float, group=None, sumsq_fn=None, scale_fn=None) -> torch.Tensor:
+    """Clip one model's gradients over the ranks of `group` to `max_norm` together, in place.
+
+    `replicated`: gradients every rank holds alike (data-parallel ones after their all-reduce;
+    the router and the shared experts); `sharded`: those of this rank's own parameters (its
+    routed experts).  The norm counts the replicated ones once and every rank's sharded ones:
+    one all-reduce of a single fp64 sum.  Either list may be empty, not both.  Returns the norm
+    before, [1] fp32.
+
+    `sumsq_fn(grads)` and `scale_fn(grads, sumsq, max_norm)` compute the sum of squares and scale;
+    the defaults are the library's kernels (`clip.grad_sumsq`, `clip.scale_grads`)."""
+    if sumsq_fn is None or scale_fn is None:
+        from . import clip
+        sumsq_fn, scale_fn = sumsq_fn or clip.grad_sumsq, scale_fn or clip.scale_grads
+    replicated, sharded = list(replicated), list(sharded)
+    if not replicated and not sharded:
+        raise ValueError("no gradients")
+    dev = (replicated or sharded)[0].device
+    # a rank without sharded gradients takes part in the all-reduce all the same
+    total = sumsq_fn(sharded) if sharded else torch.zeros(1, dtype=torch.float64, device=dev)
+    dist.all_reduce(total, group=group)
+    if replicated:
+        total = total + sumsq_fn(replicated)
+    return scale_fn(replicated + sharded, total, max_norm)

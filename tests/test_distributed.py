@@ -98,3 +98,58 @@ def test_sharded_balance_statistics_match_the_full_batch(bounds):
         assert aux_g == pytest.approx(full.aux, rel=1e-12)
     # routing is per token: the shards' indices are the full batch's rows
     np.testing.assert_array_equal(np.concatenate([res[0][4], res[1][4]]), full.routing.topk_idx)
+
+
+def _clip_worker(rank, world, port, q):
+    os.environ["MASTER_ADDR"] = "127.0.0.1"
+    os.environ["MASTER_PORT"] = str(port)
+    dist.init_process_group("gloo", rank=rank, world_size=world)
+    try:
+        g = torch.Generator().manual_seed(0)
+        shared = [torch.randn(5, 3, generator=g), torch.randn(7, generator=g)]
+        own = [[torch.randn(4, 2, generator=g)], []][rank]   # rank 1 holds no expert of its own
+
+        def sumsq(ts):
+            return sum(t.double().square().sum() for t in ts).reshape(1)
+
+        def scale(ts, total, max_norm):
+            norm = total.sqrt()
+            for t in ts:
+                t.mul_(min(1.0, max_norm / float(norm)))
+            return norm.float()
+
+        norm = parallel.clip_grad_norm(shared, own, 1.5, sumsq_fn=sumsq, scale_fn=scale)
+        q.put((rank, float(norm), [t.numpy() for t in shared], [t.numpy() for t in own]))
+    finally:
+        dist.destroy_process_group()
+
+
+def test_gradients_of_one_model_on_two_ranks_are_clipped_together():
+    ctx = mp.get_context("spawn")
+    q = ctx.Queue()
+    port = _free_port()
+    procs = [ctx.Process(target=_clip_worker, args=(r, 2, port, q)) for r in range(2)]
+    for p in procs:
+        p.start()
+    got = {}
+    for _ in procs:
+        r = q.get(timeout=120)
+        got[r[0]] = r[1:]
+    for p in procs:
+        p.join(60)
+        assert p.exitcode == 0
+    g = torch.Generator().manual_seed(0)
+    full = [torch.randn(5, 3, generator=g), torch.randn(7, generator=g), torch.randn(4, 2, generator=g)]
+    want = float(sum(t.double().square().sum() for t in full).sqrt())
+    assert want > 1.5
+    for r in (0, 1):
+        assert got[r][0] == pytest.approx(want, rel=1e-6)
+    for a, b, t in zip(got[0][1], got[1][1], full):
+        assert np.array_equal(a, b)                      # the replicated ones stay alike
+        assert np.allclose(a, t.numpy() * (1.5 / want), rtol=1e-6)
+    assert np.allclose(got[0][2][0], full[2].numpy() * (1.5 / want), rtol=1e-6)
+
+
+def test_clipping_over_ranks_refuses_nothing_to_clip():
+    with pytest.raises(ValueError, match="no gradients"):
+        parallel.clip_grad_norm([], [], 1.0)
