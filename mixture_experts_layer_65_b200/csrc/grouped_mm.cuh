@@ -101,9 +101,9 @@ __device__ __forceinline__ int group_of(const GroupTable& t, int G, int tile) {
 }
 
 // ------------------------------------------------------------------------ CUDA cores
-// fp32 operands, and bf16 ones whose widths or addresses TMA cannot take: fp32 FMA on
-// BM x BN tiles, a thread R x R outputs, 16-deep steps through two buffers in shared memory (the
-// next step's elements are on their way in registers while this one is computed).
+// fp32 operands: fp32 FMA (two per instruction) on BM x BN tiles, a thread R x R outputs, 16-deep
+// steps through two buffers in shared memory (the next step's elements are on their way in
+// registers while this one is computed).
 constexpr int kGsBK = 16;
 
 struct GroupedSimtArgs {
@@ -115,17 +115,21 @@ struct GroupedSimtArgs {
   int accumulate;       // wgrad: add to out
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T v) {
-  if constexpr (sizeof(T) == 2) return __bfloat162float(v);
-  else return v;
+// Two fp32 fused multiply-adds, each rounded to nearest.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
 }
 
 // OP's tile: rows of out (M index) x columns (N index), contraction index q:
 //   mm:    A[m, q] = x[row0 + m][q]       B[n, q] = W[n][q]      q < K
 //   dgrad: A[m, q] = dy[row0 + m][q]      B[n, q] = W[q][n]      q < N
 //   wgrad: A[m, q] = dy[row0 + q][m]      B[n, q] = x[row0 + q][n]   q < rows of the group
-template <typename T, int OP, int BM, int BN, int R>
+template <int OP, int BM, int BN, int R>
 __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(GroupedSimtArgs p) {
   constexpr int kThreads = BM * BN / (R * R);
   constexpr int kA = BM * kGsBK / kThreads, kB = BN * kGsBK / kThreads;   // elements a thread loads
@@ -149,16 +153,16 @@ __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(Grouped
     const int grow0 = tab.row0[g], grows = tab.row0[g + 1] - grow0;
     const int M = W ? p.N : grows;
     const int Q = OP == kGroupedMM ? p.K : OP == kGroupedDgrad ? p.N : grows;
-    const T* A = static_cast<const T*>(p.a) + (size_t)grow0 * lda;
-    const T* B = static_cast<const T*>(p.b) + (W ? (size_t)grow0 * p.K : (size_t)g * p.N * p.K);
-    T ra[kA], rb[kB];
+    const float* A = static_cast<const float*>(p.a) + (size_t)grow0 * lda;
+    const float* B = static_cast<const float*>(p.b) + (W ? (size_t)grow0 * p.K : (size_t)g * p.N * p.K);
+    float ra[kA], rb[kB];
     // consecutive threads along each operand's contiguous index
     auto fetch = [&](int q0) {
 #pragma unroll
       for (int l = 0; l < kA; ++l) {
         const int idx = tid + l * kThreads;
         const int m = W ? idx % BM : idx / kGsBK, q = W ? idx / BM : idx % kGsBK;
-        ra[l] = T(0.f);
+        ra[l] = 0.f;
         if (m0 + m < M && q0 + q < Q)
           ra[l] = W ? A[(size_t)(q0 + q) * lda + m0 + m] : A[(size_t)(m0 + m) * lda + q0 + q];
       }
@@ -166,7 +170,7 @@ __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(Grouped
       for (int l = 0; l < kB; ++l) {
         const int idx = tid + l * kThreads;
         const int n = OP == kGroupedMM ? idx / kGsBK : idx % BN, q = OP == kGroupedMM ? idx % kGsBK : idx / BN;
-        rb[l] = T(0.f);
+        rb[l] = 0.f;
         if (n0 + n < out_cols && q0 + q < Q)
           rb[l] = OP == kGroupedMM ? B[(size_t)(n0 + n) * p.K + q0 + q] : B[(size_t)(q0 + q) * p.K + n0 + n];
       }
@@ -175,20 +179,20 @@ __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(Grouped
 #pragma unroll
       for (int l = 0; l < kA; ++l) {
         const int idx = tid + l * kThreads;
-        As[buf][W ? idx / BM : idx % kGsBK][W ? idx % BM : idx / kGsBK] = to_f32(ra[l]);
+        As[buf][W ? idx / BM : idx % kGsBK][W ? idx % BM : idx / kGsBK] = ra[l];
       }
 #pragma unroll
       for (int l = 0; l < kB; ++l) {
         const int idx = tid + l * kThreads;
-        Bs[buf][OP == kGroupedMM ? idx % kGsBK : idx / BN][OP == kGroupedMM ? idx / kGsBK : idx % BN] = to_f32(rb[l]);
+        Bs[buf][OP == kGroupedMM ? idx % kGsBK : idx / BN][OP == kGroupedMM ? idx / kGsBK : idx % BN] = rb[l];
       }
     };
     // a thread's outputs: R / 4 runs of four rows (columns), BM / (R / 4) (BN / (R / 4)) apart
-    float acc[R][R];
+    float2 acc[R][R / 2];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int j = 0; j < R; ++j) acc[i][j] = 0.f;
+      for (int j = 0; j < R / 2; ++j) acc[i][j] = make_float2(0.f, 0.f);
     constexpr int kRunM = BM / (R / 4), kRunN = BN / (R / 4);
     if (Q > 0) {
       fetch(0);
@@ -201,16 +205,17 @@ __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(Grouped
         if (more) fetch(q0 + kGsBK);
 #pragma unroll
         for (int q = 0; q < kGsBK; ++q) {
-          float av[R], bv[R];
+          float av[R];
+          float2 bv[R / 2];
 #pragma unroll
           for (int i = 0; i < R; i += 4) {
             *reinterpret_cast<float4*>(&av[i]) = *reinterpret_cast<const float4*>(&As[buf][q][i / 4 * kRunM + ty * 4]);
-            *reinterpret_cast<float4*>(&bv[i]) = *reinterpret_cast<const float4*>(&Bs[buf][q][i / 4 * kRunN + tx * 4]);
+            *reinterpret_cast<float4*>(&bv[i / 2]) = *reinterpret_cast<const float4*>(&Bs[buf][q][i / 4 * kRunN + tx * 4]);
           }
 #pragma unroll
           for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int j = 0; j < R; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+            for (int j = 0; j < R / 2; ++j) acc[i][j] = fma2(make_float2(av[i], av[i]), bv[j], acc[i][j]);
         }
         if (more) {
           put(buf ^ 1);
@@ -226,14 +231,13 @@ __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(Grouped
       for (int j = 0; j < R; ++j) {
         const int n = n0 + j / 4 * kRunN + tx * 4 + j % 4;
         if (n >= out_cols) continue;
+        const float v = j & 1 ? acc[i][j / 2].y : acc[i][j / 2].x;
         if constexpr (W) {
           if (Q == 0 && p.accumulate) continue;   // nothing to add: not touched
           float* o = static_cast<float*>(p.out) + ((size_t)g * p.N + m) * p.K + n;
-          *o = p.accumulate ? *o + acc[i][j] : acc[i][j];
+          *o = p.accumulate ? *o + v : v;
         } else {
-          T* o = static_cast<T*>(p.out) + (size_t)(grow0 + m) * out_cols + n;
-          if constexpr (sizeof(T) == 2) *o = __float2bfloat16_rn(acc[i][j]);
-          else *o = acc[i][j];
+          static_cast<float*>(p.out)[(size_t)(grow0 + m) * out_cols + n] = v;
         }
       }
     }

@@ -1,9 +1,9 @@
 // moe_grouped.cu -- moe_grouped_mm, moe_grouped_mm_dgrad and moe_grouped_mm_wgrad
 // (include/moe.h): checks, the choice of kernel, TMA descriptors and the launch.
-#include <cstdlib>
 #include "op_common.cuh"
 #include "grouped_mm.cuh"
 #include "grouped_rows.cuh"
+#include "grouped_warp.cuh"
 #include "grouped_wgrad.cuh"
 
 using namespace moe;
@@ -33,29 +33,41 @@ moe_status check_shape(const Shape& s) {
   return MOE_OK;
 }
 
-// The CUDA-core kernel with BM x BN tiles and R x R outputs a thread; its tiles at most.
+// Tiles of bm x bn at most (every expert with rows has one ragged tile row).
 template <int OP>
-int64_t simt_tiles(const Shape& s, int bm, int bn) {
+int64_t tiles_of(const Shape& s, int bm, int bn) {
   const int64_t nt = ((OP == kGroupedMM ? s.n : s.k) + bn - 1) / bn;
   return OP == kGroupedWgrad ? s.G * nt * ((s.n + bm - 1) / bm)
                              : ((s.rows + bm - 1) / bm + (s.G < s.rows ? s.G : s.rows)) * nt;
 }
-template <typename T, int OP, int BM, int BN, int R>
+
+// fp32: the largest tiles that still give every SM work for two CTAs (one at 64 x 64).
+template <int OP, int BM, int BN, int R>
 cudaError_t launch_simt_tile(const GroupedSimtArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
   constexpr int kThreads = BM * BN / (R * R);
-  const int64_t tiles = simt_tiles<OP>(s, BM, BN), most = (int64_t)n_sms * (1024 / kThreads);
-  return launch_pdl(grouped_simt_kernel<T, OP, BM, BN, R>, dim3((unsigned)(tiles < most ? tiles : most)),
+  const int64_t tiles = tiles_of<OP>(s, BM, BN), most = (int64_t)n_sms * (1024 / kThreads);
+  return launch_pdl(grouped_simt_kernel<OP, BM, BN, R>, dim3((unsigned)(tiles < most ? tiles : most)),
                     dim3(kThreads), 0, st, a);
 }
-template <typename T, int OP>
+template <int OP>
 cudaError_t launch_simt(const GroupedSimtArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
-  static const int force = getenv("MOE_SIMT") ? atoi(getenv("MOE_SIMT")) : 0;
-  if (force == 128) return launch_simt_tile<T, OP, 128, 128, 8>(a, s, n_sms, st);
-  if (force == 64) return launch_simt_tile<T, OP, 64, 64, 4>(a, s, n_sms, st);
-  if (force == 32) return launch_simt_tile<T, OP, 32, 32, 4>(a, s, n_sms, st);
-  if (simt_tiles<OP>(s, 128, 128) >= 2 * n_sms) return launch_simt_tile<T, OP, 128, 128, 8>(a, s, n_sms, st);
-  if (simt_tiles<OP>(s, 64, 64) >= n_sms) return launch_simt_tile<T, OP, 64, 64, 4>(a, s, n_sms, st);
-  return launch_simt_tile<T, OP, 32, 32, 4>(a, s, n_sms, st);
+  if (tiles_of<OP>(s, 128, 128) >= 2 * n_sms) return launch_simt_tile<OP, 128, 128, 8>(a, s, n_sms, st);
+  if (tiles_of<OP>(s, 64, 64) >= n_sms) return launch_simt_tile<OP, 64, 64, 4>(a, s, n_sms, st);
+  return launch_simt_tile<OP, 32, 32, 4>(a, s, n_sms, st);
+}
+
+// bf16 that TMA cannot take.
+template <int OP, int BM, int BN, int WM, int WN>
+cudaError_t launch_warp_tile(const GroupedWarpArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
+  constexpr int kThreads = (BM / WM) * (BN / WN) * 32;
+  const int64_t tiles = tiles_of<OP>(s, BM, BN), most = (int64_t)n_sms * (512 / kThreads);
+  return launch_pdl(grouped_warp_kernel<OP, BM, BN, WM, WN, 512 / kThreads>, dim3((unsigned)(tiles < most ? tiles : most)),
+                    dim3(kThreads), 0, st, a);
+}
+template <int OP>
+cudaError_t launch_warp(const GroupedWarpArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
+  if (tiles_of<OP>(s, 128, 128) >= n_sms) return launch_warp_tile<OP, 128, 128, 64, 32>(a, s, n_sms, st);
+  return launch_warp_tile<OP, 64, 64, 32, 32>(a, s, n_sms, st);
 }
 
 // Clusters of `kernel` that can be resident at once on the current device (asked for once per
@@ -156,9 +168,14 @@ moe_status product(const void* a, const void* b, const int32_t* counts, const Sh
   if (s.dtype == MOE_BF16 && s.n % 8 == 0 && s.k % 8 == 0 && s.rows > 0 && aligned16(a) && aligned16(b) &&
       aligned16(out))
     return launch_tc<OP>(a, b, counts, s, accumulate, out, device, n_sms, st);
-  GroupedSimtArgs p{a, b, counts, out, s.G, (int)s.rows, s.n, s.k, accumulate};
-  MOE_CUDA((s.dtype == MOE_BF16 ? launch_simt<__nv_bfloat16, OP>(p, s, n_sms, st)
-                                : launch_simt<float, OP>(p, s, n_sms, st)));
+  if (s.dtype == MOE_BF16) {
+    GroupedWarpArgs p{static_cast<const __nv_bfloat16*>(a), static_cast<const __nv_bfloat16*>(b), counts, out, s.G,
+                      (int)s.rows, s.n, s.k, accumulate};
+    MOE_CUDA(launch_warp<OP>(p, s, n_sms, st));
+  } else {
+    GroupedSimtArgs p{a, b, counts, out, s.G, (int)s.rows, s.n, s.k, accumulate};
+    MOE_CUDA(launch_simt<OP>(p, s, n_sms, st));
+  }
   return MOE_OK;
 }
 
