@@ -103,7 +103,8 @@ __device__ __forceinline__ int group_of(const GroupTable& t, int G, int tile) {
 // ------------------------------------------------------------------------ CUDA cores
 // fp32 operands: fp32 FMA (two per instruction) on BM x BN tiles, a thread R x R outputs, 16-deep
 // steps through two buffers in shared memory (the next step's elements are on their way in
-// registers while this one is computed).
+// registers while this one is computed).  V elements a load: 4 when the widths are multiples of 4
+// and the buffers 16-byte aligned, else 1.
 constexpr int kGsBK = 16;
 
 struct GroupedSimtArgs {
@@ -129,10 +130,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 //   mm:    A[m, q] = x[row0 + m][q]       B[n, q] = W[n][q]      q < K
 //   dgrad: A[m, q] = dy[row0 + m][q]      B[n, q] = W[q][n]      q < N
 //   wgrad: A[m, q] = dy[row0 + q][m]      B[n, q] = x[row0 + q][n]   q < rows of the group
-template <int OP, int BM, int BN, int R>
+template <int OP, int BM, int BN, int R, int V>
 __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(GroupedSimtArgs p) {
   constexpr int kThreads = BM * BN / (R * R);
-  constexpr int kA = BM * kGsBK / kThreads, kB = BN * kGsBK / kThreads;   // elements a thread loads
+  constexpr int kA = BM * kGsBK / kThreads / V, kB = BN * kGsBK / kThreads / V;   // loads of a thread
   constexpr bool W = OP == kGroupedWgrad;
   pdl_launch_dependents();
   pdl_wait();
@@ -155,36 +156,46 @@ __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(Grouped
     const int Q = OP == kGroupedMM ? p.K : OP == kGroupedDgrad ? p.N : grows;
     const float* A = static_cast<const float*>(p.a) + (size_t)grow0 * lda;
     const float* B = static_cast<const float*>(p.b) + (W ? (size_t)grow0 * p.K : (size_t)g * p.N * p.K);
-    float ra[kA], rb[kB];
+    float ra[kA][V], rb[kB][V];
     // consecutive threads along each operand's contiguous index
+    constexpr bool kAMn = W, kBMn = OP != kGroupedMM;   // contiguous along the output index
+    constexpr int kQv = kGsBK / V;
+    auto load = [&](float (&r)[V], const float* src, bool in) {
+      if constexpr (V == 4) {
+        const float4 v = in ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+        r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
+      } else {
+        r[0] = in ? *src : 0.f;
+      }
+    };
     auto fetch = [&](int q0) {
 #pragma unroll
       for (int l = 0; l < kA; ++l) {
-        const int idx = tid + l * kThreads;
-        const int m = W ? idx % BM : idx / kGsBK, q = W ? idx / BM : idx % kGsBK;
-        ra[l] = 0.f;
-        if (m0 + m < M && q0 + q < Q)
-          ra[l] = W ? A[(size_t)(q0 + q) * lda + m0 + m] : A[(size_t)(m0 + m) * lda + q0 + q];
+        const int i = tid + l * kThreads;
+        const int m = m0 + (kAMn ? i % (BM / V) * V : i / kQv), q = q0 + (kAMn ? i / (BM / V) : i % kQv * V);
+        load(ra[l], A + (kAMn ? (size_t)q * lda + m : (size_t)m * lda + q), m < M && q < Q);
       }
 #pragma unroll
       for (int l = 0; l < kB; ++l) {
-        const int idx = tid + l * kThreads;
-        const int n = OP == kGroupedMM ? idx / kGsBK : idx % BN, q = OP == kGroupedMM ? idx % kGsBK : idx / BN;
-        rb[l] = 0.f;
-        if (n0 + n < out_cols && q0 + q < Q)
-          rb[l] = OP == kGroupedMM ? B[(size_t)(n0 + n) * p.K + q0 + q] : B[(size_t)(q0 + q) * p.K + n0 + n];
+        const int i = tid + l * kThreads;
+        const int n = n0 + (kBMn ? i % (BN / V) * V : i / kQv), q = q0 + (kBMn ? i / (BN / V) : i % kQv * V);
+        load(rb[l], B + (kBMn ? (size_t)q * p.K + n : (size_t)n * p.K + q), n < out_cols && q < Q);
       }
     };
     auto put = [&](int buf) {
 #pragma unroll
       for (int l = 0; l < kA; ++l) {
-        const int idx = tid + l * kThreads;
-        As[buf][W ? idx / BM : idx % kGsBK][W ? idx % BM : idx / kGsBK] = ra[l];
+        const int i = tid + l * kThreads;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          As[buf][kAMn ? i / (BM / V) : i % kQv * V + v][kAMn ? i % (BM / V) * V + v : i / kQv] = ra[l][v];
       }
 #pragma unroll
       for (int l = 0; l < kB; ++l) {
-        const int idx = tid + l * kThreads;
-        Bs[buf][OP == kGroupedMM ? idx % kGsBK : idx / BN][OP == kGroupedMM ? idx / kGsBK : idx % BN] = rb[l];
+        const int i = tid + l * kThreads;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          Bs[buf][kBMn ? i / (BN / V) : i % kQv * V + v][kBMn ? i % (BN / V) * V + v : i / kQv] = rb[l][v];
       }
     };
     // a thread's outputs: R / 4 runs of four rows (columns), BM / (R / 4) (BN / (R / 4)) apart
