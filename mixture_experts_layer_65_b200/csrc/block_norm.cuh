@@ -12,9 +12,12 @@
 //   d_pre  = sum_t du xh,  d_post = sum_t g gate yh,
 //   d_gate = sum_t g p (per channel) or sum_j g p (per token)
 //
-// One CTA of TPR threads holds a row in registers (NV accesses of V elements a thread), so
-// each tensor crosses HBM once; every sum and statistic is fp32.  u and the statistic s(r)
-// come from r before it is rounded to its type (one rounding less than reading it back).
+// A row belongs to one CTA (to one warp up to 64 accesses of V elements), so each tensor crosses
+// HBM once.  CTAs are persistent: parameters stay in registers, the next two rows are on their
+// way to shared memory while this one is reduced (each thread copies, and later reads, its own
+// 16 bytes, so nothing waits for another thread's copies), and the backward's column sums are
+// kept per CTA.  Every sum and statistic is fp32.  u and the statistic s(r) come from r before
+// it is rounded to its type (one rounding less than reading it back).
 #pragma once
 
 #include "ptx.cuh"
@@ -61,14 +64,16 @@ struct BlockNormBwdArgs {
   float beta;
 };
 
-// V consecutive elements of T widened to fp32, and back with one rounding.
+// V consecutive elements of T: as loaded, widened to fp32, and stored with one rounding.
 template <typename T, int V>
 struct RowVec;
 template <>
 struct RowVec<__nv_bfloat16, 8> {
-  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[8]) {
-    bf16x8_to_f32(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i), f);
+  using Raw = uint4;
+  static __device__ __forceinline__ Raw load(const void* p, int64_t i) {
+    return *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
   }
+  static __device__ __forceinline__ void widen(const Raw& r, float (&f)[8]) { bf16x8_to_f32(r, f); }
   static __device__ __forceinline__ void store(void* p, int64_t i, const float (&f)[8]) {
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) =
         make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
@@ -77,9 +82,12 @@ struct RowVec<__nv_bfloat16, 8> {
 };
 template <>
 struct RowVec<float, 4> {
-  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[4]) {
-    const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+  using Raw = float4;
+  static __device__ __forceinline__ Raw load(const void* p, int64_t i) {
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  }
+  static __device__ __forceinline__ void widen(const Raw& r, float (&f)[4]) {
+    f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w;
   }
   static __device__ __forceinline__ void store(void* p, int64_t i, const float (&f)[4]) {
     *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(f[0], f[1], f[2], f[3]);
@@ -87,18 +95,18 @@ struct RowVec<float, 4> {
 };
 template <>
 struct RowVec<__nv_bfloat16, 1> {
-  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[1]) {
-    f[0] = __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  }
+  using Raw = __nv_bfloat16;
+  static __device__ __forceinline__ Raw load(const void* p, int64_t i) { return static_cast<const __nv_bfloat16*>(p)[i]; }
+  static __device__ __forceinline__ void widen(const Raw& r, float (&f)[1]) { f[0] = __bfloat162float(r); }
   static __device__ __forceinline__ void store(void* p, int64_t i, const float (&f)[1]) {
     static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(f[0]);
   }
 };
 template <>
 struct RowVec<float, 1> {
-  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[1]) {
-    f[0] = static_cast<const float*>(p)[i];
-  }
+  using Raw = float;
+  static __device__ __forceinline__ Raw load(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+  static __device__ __forceinline__ void widen(const Raw& r, float (&f)[1]) { f[0] = r; }
   static __device__ __forceinline__ void store(void* p, int64_t i, const float (&f)[1]) {
     static_cast<float*>(p)[i] = f[0];
   }
@@ -119,221 +127,417 @@ __device__ __forceinline__ void load_param(const float* p, int i, float (&f)[V])
   }
 }
 
-// Sum of v over the CTA's TPR threads, the same value in each (lanes by butterfly, then the
-// warps in order).  The next call that uses `buf` comes after another call's barrier.
-template <int TPR>
+// V consecutive fp32 values stored.
+template <int V>
+__device__ __forceinline__ void store_f32(float* p, const float (&f)[V]) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int q = 0; q < V / 4; ++q)
+      *(reinterpret_cast<float4*>(p) + q) = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < V; ++q) p[q] = f[q];
+  }
+}
+
+// Sum of v over a row's threads, the same value in each: lanes by butterfly, then (WARP_ROW:
+// a warp has the row to itself) the CTA's warps by another.  The next call that uses `buf` comes
+// after another call's barrier.
+template <bool WARP_ROW>
 __device__ __forceinline__ float row_sum(float v, float* buf) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (TPR > 32) {
-    constexpr int kWarps = TPR / 32;
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  if constexpr (!WARP_ROW) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.f;
+    v = lane < (int)(blockDim.x >> 5) ? buf[lane] : 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += buf[w];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   }
   return v;
 }
 
-template <typename T, int V, int NV, int TPR>
-__global__ void __launch_bounds__(TPR) block_norm_kernel(BlockNormArgs a) {
+// Threads of a kernel: MAXT = 32 stands for one warp per row, eight rows a CTA; else the CTA has
+// as many threads as a row needs, at most MAXT.
+constexpr int kNormWarps = 8;
+constexpr int kNormRing = 3;   // rows in shared memory: the one at work and two on their way
+__host__ __device__ constexpr int norm_max_threads(int maxt) { return maxt == 32 ? 32 * kNormWarps : maxt; }
+// Parameters are kept in registers up to 512 threads a CTA (128 registers a thread).
+__host__ __device__ constexpr bool norm_keeps(int maxt) { return maxt <= 512; }
+// Rows go through the ring there too, when they are read 16 bytes at a time.
+__host__ __device__ constexpr bool norm_rings(int v, int maxt) { return v > 1 && norm_keeps(maxt); }
+__host__ __device__ constexpr size_t norm_ring_bytes(int streams, int nv, int threads) {
+  return (size_t)kNormRing * streams * nv * threads * 16;
+}
+
+// K row streams of one thread, NV accesses each: through the ring, or (no ring) to registers: one
+// row ahead (EARLY) or when the row's turn comes.  An absent stream has a null pointer.
+template <typename T, int V, int NV, int K, bool RING, bool EARLY>
+struct RowStreams {
   using RV = RowVec<T, V>;
-  pdl_launch_dependents();
-  pdl_wait();
-  __shared__ float red[2][32];
-  const int64_t row = blockIdx.x;
-  const int64_t base = row * a.d;
-  const float inv_d = 1.0f / (float)a.d;
-  float r[NV][V], y[NV][V];
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (threadIdx.x + i * TPR) * V;
-    if (c < a.d) {
-      RV::load(a.x, base + c, r[i]);
-      if (a.y) RV::load(a.y, base + c, y[i]);
+  using Raw = typename RV::Raw;
+  const void* src[K];
+  uint32_t smem;      // this thread's first 16 bytes
+  uint32_t pitch;     // bytes between a thread's slots
+  int slot;           // of the row at work
+  Raw cur[RING ? 1 : K][NV], coming[EARLY ? K : 1][NV];
+
+  __device__ __forceinline__ void init(uint8_t* ring) {
+    if constexpr (RING) {
+      smem = smem_u32(ring) + threadIdx.x * 16;
+      pitch = blockDim.x * 16;
+      slot = 0;
     }
   }
-  if (a.y) {
-    float s = 1.0f;
-    if (a.w_post) {
+  // Ask for a row (col(i): this thread's columns) into the ring, `ahead` rows behind the one at
+  // work; a row past the end only keeps the count.
+  template <class C>
+  __device__ __forceinline__ void ask(int64_t row, int64_t T_, int d, int ahead, C&& col) {
+    if constexpr (RING) {
+      if (row < T_) {
+        const int to = (slot + ahead) % kNormRing;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (src[k])
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+              if (col(i) < d)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem + ((to * K + k) * NV + i) * pitch),
+                             "l"(static_cast<const T*>(src[k]) + row * d + col(i))
+                             : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    } else if constexpr (EARLY) {
+      if (row < T_ && ahead == 0)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (src[k])
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+              if (col(i) < d) coming[k][i] = RV::load(src[k], row * d + col(i));
+    }
+  }
+  // The row at work is there.
+  template <class C>
+  __device__ __forceinline__ void take(int64_t row, int d, C&& col) {
+    if constexpr (RING) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kNormRing - 1) : "memory");
+    } else if constexpr (EARLY) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) cur[k][i] = coming[k][i];
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (src[k])
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (col(i) < d) cur[k][i] = RV::load(src[k], row * d + col(i));
+    }
+  }
+  __device__ __forceinline__ void get(int k, int i, float (&f)[V]) const {
+    if constexpr (RING) {
+      uint32_t x, y, z, w;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
+                   : "r"(smem + ((slot * K + k) * NV + i) * pitch)
+                   : "memory");
+      if constexpr (sizeof(T) == 2) {
+        RV::widen(make_uint4(x, y, z, w), f);
+      } else {
+        f[0] = __uint_as_float(x); f[1] = __uint_as_float(y); f[2] = __uint_as_float(z); f[3] = __uint_as_float(w);
+      }
+    } else {
+      RV::widen(cur[k][i], f);
+    }
+  }
+  __device__ __forceinline__ void next() {
+    if constexpr (RING) slot = slot + 1 == kNormRing ? 0 : slot + 1;
+  }
+};
+
+// The columns' parameters of one thread: post weight times channel gate, and the pre weight, in
+// registers (KEEP) or read again for every row.
+template <int V, int NV, bool KEEP>
+struct RowParams {
+  const float *w_post, *gate_ch, *w_pre;   // nullptr: ones
+  float wq[KEEP ? NV : 1][V], wp[KEEP ? NV : 1][V];
+
+  __device__ __forceinline__ void scale_of(int c, float (&w)[V]) const {
+#pragma unroll
+    for (int j = 0; j < V; ++j) w[j] = 1.0f;
+    if (w_post) load_param<V>(w_post, c, w);
+    if (gate_ch) {
+      float gc[V];
+      load_param<V>(gate_ch, c, gc);
+#pragma unroll
+      for (int j = 0; j < V; ++j) w[j] *= gc[j];
+    }
+  }
+  template <class C>
+  __device__ __forceinline__ void init(int d, C&& col) {
+    if constexpr (KEEP) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if ((threadIdx.x + i * TPR) * V < a.d)
-#pragma unroll
-          for (int j = 0; j < V; ++j) ss = fmaf(y[i][j], y[i][j], ss);
-      s = __frsqrt_rn(fmaf(row_sum<TPR>(ss, red[0]), inv_d, a.eps));
-      if (threadIdx.x == 0) a.s_post[row] = s;
-    }
-    const float gt = a.gate_kind == kGateToken ? __ldg(a.gate + row) : 1.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (threadIdx.x + i * TPR) * V;
-      if (c < a.d) {
-        float w[V], gc[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) w[j] = gc[j] = 1.0f;
-        if (a.w_post) load_param<V>(a.w_post, c, w);
-        if (a.gate_kind == kGateChannel) load_param<V>(a.gate, c, gc);
-#pragma unroll
-        for (int j = 0; j < V; ++j) r[i][j] = fmaf(a.beta, r[i][j], y[i][j] * s * w[j] * (gc[j] * gt));
-        RV::store(a.r, base + c, r[i]);
-      }
+        if (col(i) < d) {
+          scale_of(col(i), wq[i]);
+          if (w_pre) load_param<V>(w_pre, col(i), wp[i]);
+        }
     }
   }
-  if (a.w_pre) {
-    ss = 0.f;
+  __device__ __forceinline__ void post(int i, int c, float (&w)[V]) const {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) w[j] = wq[i][j];
+    } else {
+      scale_of(c, w);
+    }
+  }
+  __device__ __forceinline__ void pre(int i, int c, float (&w)[V]) const {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) w[j] = wp[i][j];
+    } else {
+      load_param<V>(w_pre, c, w);
+    }
+  }
+};
+
+template <typename T, int V, int NV, int MAXT>
+__global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_kernel(BlockNormArgs a) {
+  using RV = RowVec<T, V>;
+  constexpr bool kWarpRow = MAXT == 32;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float red[2][2][32];   // two rows' sums: a row's may still be read while the next's come
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
+  const int tpr = kWarpRow ? 32 : blockDim.x;
+  const int64_t step = kWarpRow ? (int64_t)gridDim.x * kNormWarps : gridDim.x;
+  const float inv_d = 1.0f / (float)a.d;
+  auto col = [&](int i) { return (tid + i * tpr) * V; };
+  int64_t row = kWarpRow ? (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5) : blockIdx.x;
+  constexpr bool kRing = norm_rings(V, MAXT), kEarly = !kRing && norm_keeps(MAXT);
+  RowStreams<T, V, NV, 2, kRing, kEarly> in{{a.x, a.y}};
+  in.init(ring);
+#pragma unroll
+  for (int i = 0; i < kNormRing - 1; ++i) in.ask(row + i * step, a.T, a.d, i, col);
+  RowParams<V, NV, norm_keeps(MAXT)> par{a.w_post, a.gate_kind == kGateChannel ? a.gate : nullptr, a.w_pre};
+  par.init(a.d, col);
+  // the row's own parameter is loaded a row ahead too
+  auto token_gate = [&](int64_t i) { return a.gate_kind == kGateToken && i < a.T ? __ldg(a.gate + i) : 1.0f; };
+  float gt_next = token_gate(row);
+  for (int odd = 0; row < a.T; row += step, odd ^= 1) {
+    in.ask(row + (kNormRing - 1) * step, a.T, a.d, kNormRing - 1, col);
+    in.take(row, a.d, col);
+    if (kEarly) in.ask(row + step, a.T, a.d, 0, col);
+    const float gt = gt_next;
+    gt_next = token_gate(row + step);
+    const int64_t base = row * a.d;
+    float r[NV][V], p[NV][V];
+    float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if ((threadIdx.x + i * TPR) * V < a.d)
+      if (col(i) < a.d) {
+        in.get(0, i, r[i]);
+        if (a.y) {
+          in.get(1, i, p[i]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) ss = fmaf(r[i][j], r[i][j], ss);
-    const float s = __frsqrt_rn(fmaf(row_sum<TPR>(ss, red[1]), inv_d, a.eps));
-    if (threadIdx.x == 0) a.s_pre[row] = s;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (threadIdx.x + i * TPR) * V;
-      if (c < a.d) {
-        float w[V];
-        load_param<V>(a.w_pre, c, w);
-#pragma unroll
-        for (int j = 0; j < V; ++j) w[j] *= r[i][j] * s;
-        RV::store(a.u, base + c, w);
+          for (int j = 0; j < V; ++j) ss = fmaf(p[i][j], p[i][j], ss);
+        }
       }
+    in.next();
+    if (a.y) {
+      float s = 1.0f;
+      if (a.w_post) {
+        s = __frsqrt_rn(fmaf(row_sum<kWarpRow>(ss, red[odd][0]), inv_d, a.eps));
+        if (tid == 0) a.s_post[row] = s;
+      }
+      s *= gt;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < a.d) {
+          float w[V];
+          par.post(i, col(i), w);
+#pragma unroll
+          for (int j = 0; j < V; ++j) r[i][j] = fmaf(a.beta, r[i][j], p[i][j] * s * w[j]);
+          RV::store(a.r, base + col(i), r[i]);
+        }
+    }
+    if (a.w_pre) {
+      ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < a.d)
+#pragma unroll
+          for (int j = 0; j < V; ++j) ss = fmaf(r[i][j], r[i][j], ss);
+      const float s = __frsqrt_rn(fmaf(row_sum<kWarpRow>(ss, red[odd][1]), inv_d, a.eps));
+      if (tid == 0) a.s_pre[row] = s;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < a.d) {
+          float w[V];
+          par.pre(i, col(i), w);
+#pragma unroll
+          for (int j = 0; j < V; ++j) w[j] *= r[i][j] * s;
+          RV::store(a.u, base + col(i), w);
+        }
     }
   }
 }
 
-// The CTA walks rows blockIdx.x, blockIdx.x + gridDim.x, ... and keeps its columns' sums in
-// registers, so the parameter gradients cost one [gridDim.x, d] array of partial sums.
-template <typename T, int V, int NV, int TPR>
-__global__ void __launch_bounds__(TPR) block_norm_bwd_kernel(BlockNormBwdArgs a) {
+// Column sums of the warps of a CTA (one warp per row), added in order by the CTA.
+template <int V, int NV>
+__device__ __forceinline__ void cta_columns(float (&acc)[NV][V], float* sh, float* part, int d) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kWidth = NV * V * 32;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) sh[warp * kWidth + (lane + i * 32) * V + j] = acc[i][j];
+  __syncthreads();
+  for (int c = threadIdx.x; c < d; c += 32 * kNormWarps) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kNormWarps; ++w) v += sh[w * kWidth + c];
+    part[c] = v;
+  }
+}
+
+// As block_norm_kernel; the columns' sums stay in registers over a CTA's (warp's) rows, so the
+// parameter gradients cost one [gridDim.x, d] array of partial sums each.
+template <typename T, int V, int NV, int MAXT>
+__global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_bwd_kernel(BlockNormBwdArgs a) {
   using RV = RowVec<T, V>;
+  constexpr bool kWarpRow = MAXT == 32;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float red[2][2][32];
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ float red[2][2][32];   // two rows' sums: a row's may still be read while the next's come
-  int par = 0;
+  const int tid = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
+  const int tpr = kWarpRow ? 32 : blockDim.x;
+  const int64_t step = kWarpRow ? (int64_t)gridDim.x * kNormWarps : gridDim.x;
   const float inv_d = 1.0f / (float)a.d;
+  auto col = [&](int i) { return (tid + i * tpr) * V; };
+  int64_t row = kWarpRow ? (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5) : blockIdx.x;
+  enum { kR = 0, kDu = 1, kDr = 2, kY = 3 };
+  RowStreams<T, V, NV, 4, norm_rings(V, MAXT), false> in{{a.w_pre ? a.r : nullptr, a.w_pre ? a.du : nullptr, a.dr, a.y}};
+  in.init(ring);
+#pragma unroll
+  for (int i = 0; i < kNormRing - 1; ++i) in.ask(row + i * step, a.T, a.d, i, col);
+  RowParams<V, NV, norm_keeps(MAXT)> par{a.w_post, a.gate_kind == kGateChannel ? a.gate : nullptr, a.w_pre};
+  par.init(a.d, col);
   float acc_pre[NV][V], acc_s[NV][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < V; ++j) acc_pre[i][j] = acc_s[i][j] = 0.f;
-  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, par ^= 1) {
+  // the row's own values are loaded a row ahead too
+  auto own = [&](const float* p, bool on, int64_t i) { return on && i < a.T ? __ldg(p + i) : 1.0f; };
+  float pre_next = own(a.s_pre, a.w_pre, row), post_next = own(a.s_post, a.w_post, row);
+  float gt_next = own(a.gate, a.gate_kind == kGateToken, row);
+  for (int odd = 0; row < a.T; row += step, odd ^= 1) {
+    in.ask(row + (kNormRing - 1) * step, a.T, a.d, kNormRing - 1, col);
+    in.take(row, a.d, col);
+    const float s_pre = pre_next, s_post = post_next, gt = gt_next;
+    pre_next = own(a.s_pre, a.w_pre, row + step);
+    post_next = own(a.s_post, a.w_post, row + step);
+    gt_next = own(a.gate, a.gate_kind == kGateToken, row + step);
     const int64_t base = row * a.d;
-    float g[NV][V], y[NV][V];
+    float g[NV][V];
+    float mean = 0.f, s = s_pre;
     if (a.w_pre) {
-      float xh[NV][V], dh[NV][V];
-      const float s = __ldg(a.s_pre + row);
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (threadIdx.x + i * TPR) * V;
-        if (c < a.d) {
-          RV::load(a.r, base + c, xh[i]);
-          RV::load(a.du, base + c, dh[i]);
-          if (a.dr) RV::load(a.dr, base + c, g[i]);
-          if (a.y) RV::load(a.y, base + c, y[i]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (threadIdx.x + i * TPR) * V;
-        if (c < a.d) {
-          float w[V];
-          load_param<V>(a.w_pre, c, w);
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < a.d) {
+          float xh[V], dh[V], w[V];
+          in.get(kR, i, xh);
+          in.get(kDu, i, dh);
+          par.pre(i, col(i), w);
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            xh[i][j] *= s;
-            acc_pre[i][j] = fmaf(dh[i][j], xh[i][j], acc_pre[i][j]);
-            dh[i][j] *= w[j];
-            sum = fmaf(dh[i][j], xh[i][j], sum);
+            const float t = dh[j] * (xh[j] * s);
+            acc_pre[i][j] += t;
+            sum = fmaf(t, w[j], sum);
           }
         }
-      }
-      const float mean = row_sum<TPR>(sum, red[par][0]) * inv_d;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float t = s * (dh[i][j] - xh[i][j] * mean);
-          g[i][j] = a.dr ? g[i][j] + t : t;
-        }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (threadIdx.x + i * TPR) * V;
-        if (c < a.d) {
-          RV::load(a.dr, base + c, g[i]);
-          if (a.y) RV::load(a.y, base + c, y[i]);
-        }
-      }
+      mean = row_sum<kWarpRow>(sum, red[odd][0]) * inv_d;
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (threadIdx.x + i * TPR) * V;
-      if (c < a.d) {
+    for (int i = 0; i < NV; ++i)
+      if (col(i) < a.d) {
+        if (a.dr) {
+          in.get(kDr, i, g[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) g[i][j] = 0.f;
+        }
+        if (a.w_pre) {
+          float xh[V], dh[V], w[V];
+          in.get(kR, i, xh);
+          in.get(kDu, i, dh);
+          par.pre(i, col(i), w);
+#pragma unroll
+          for (int j = 0; j < V; ++j) g[i][j] = fmaf(s, fmaf(-mean, xh[j] * s, dh[j] * w[j]), g[i][j]);
+        }
         float dx[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) dx[j] = a.beta * g[i][j];
-        RV::store(a.dx, base + c, dx);
+        RV::store(a.dx, base + col(i), dx);
       }
-    }
     if (a.y) {
-      const float s = a.w_post ? __ldg(a.s_post + row) : 1.0f;
-      const float gt = a.gate_kind == kGateToken ? __ldg(a.gate + row) : 1.0f;
+      s = s_post;
       float sum = 0.f;
-      // y becomes yh, g becomes g times the channel gate and w_post (q without the token gate)
+      // g becomes g times the channel gate and w_post (q without the token gate)
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (threadIdx.x + i * TPR) * V;
-        if (c < a.d) {
-          float w[V], gc[V];
-#pragma unroll
-          for (int j = 0; j < V; ++j) w[j] = gc[j] = 1.0f;
-          if (a.w_post) load_param<V>(a.w_post, c, w);
-          if (a.gate_kind == kGateChannel) load_param<V>(a.gate, c, gc);
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < a.d) {
+          float yh[V], w[V];
+          in.get(kY, i, yh);
+          par.post(i, col(i), w);
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            y[i][j] *= s;
-            acc_s[i][j] = fmaf(g[i][j] * gt, y[i][j], acc_s[i][j]);
-            g[i][j] *= gc[j] * w[j];
-            sum = fmaf(g[i][j], y[i][j], sum);
+            yh[j] *= s;
+            acc_s[i][j] = fmaf(g[i][j] * gt, yh[j], acc_s[i][j]);
+            g[i][j] *= w[j];
+            sum = fmaf(g[i][j], yh[j], sum);
           }
         }
-      }
-      float mean = 0.f;
-      if (a.w_post || a.gate_kind == kGateToken) {   // uniform over the CTA
-        sum = row_sum<TPR>(sum, red[par][1]);
-        if (a.gate_kind == kGateToken && threadIdx.x == 0) a.d_gate_tok[row] = sum;
+      mean = 0.f;
+      if (a.w_post || a.gate_kind == kGateToken) {   // the same for every thread
+        sum = row_sum<kWarpRow>(sum, red[odd][1]);
+        if (a.gate_kind == kGateToken && tid == 0) a.d_gate_tok[row] = sum;
         if (a.w_post) mean = sum * inv_d;
       }
       const float sg = s * gt;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (threadIdx.x + i * TPR) * V;
-        if (c < a.d) {
-          float dy[V];
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < a.d) {
+          float yh[V];
+          in.get(kY, i, yh);
 #pragma unroll
-          for (int j = 0; j < V; ++j) dy[j] = sg * (g[i][j] - y[i][j] * mean);
-          RV::store(a.dy, base + c, dy);
+          for (int j = 0; j < V; ++j) yh[j] = sg * fmaf(-mean, yh[j] * s, g[i][j]);
+          RV::store(a.dy, base + col(i), yh);
         }
-      }
     }
+    in.next();
   }
+  const int64_t o = (int64_t)blockIdx.x * a.d;
+  if constexpr (kWarpRow) {
+    __shared__ float sh[kNormWarps * NV * V * 32];
+    if (a.part_pre) cta_columns<V, NV>(acc_pre, sh, a.part_pre + o, a.d);
+    if (a.part_s) cta_columns<V, NV>(acc_s, sh, a.part_s + o, a.d);
+  } else {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (threadIdx.x + i * TPR) * V;
-    if (c < a.d) {
-      const int64_t o = (int64_t)blockIdx.x * a.d + c;
-      if (a.part_pre) RowVec<float, V % 4 == 0 ? 4 : 1>::store(a.part_pre, o, *reinterpret_cast<float(*)[V % 4 == 0 ? 4 : 1]>(&acc_pre[i][0]));
-      if (a.part_s) RowVec<float, V % 4 == 0 ? 4 : 1>::store(a.part_s, o, *reinterpret_cast<float(*)[V % 4 == 0 ? 4 : 1]>(&acc_s[i][0]));
-      if constexpr (V == 8) {
-        if (a.part_pre) RowVec<float, 4>::store(a.part_pre, o + 4, *reinterpret_cast<float(*)[4]>(&acc_pre[i][4]));
-        if (a.part_s) RowVec<float, 4>::store(a.part_s, o + 4, *reinterpret_cast<float(*)[4]>(&acc_s[i][4]));
+    for (int i = 0; i < NV; ++i)
+      if (col(i) < a.d) {
+        if (a.part_pre) store_f32<V>(a.part_pre + o + col(i), acc_pre[i]);
+        if (a.part_s) store_f32<V>(a.part_s + o + col(i), acc_s[i]);
       }
-    }
   }
 }
 

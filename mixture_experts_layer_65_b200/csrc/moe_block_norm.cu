@@ -7,40 +7,64 @@ using namespace moe;
 
 namespace {
 
-// Call f(V, NV, TPR) for rows of d elements of T: 16-byte accesses when d is a multiple of
-// their elements and every row pointer is 16-byte aligned, else one element an access; the
-// fewest threads (64 to 1024) that hold a row in two 16-byte accesses each (eight single
-// elements), more accesses a thread only for rows past 1024 threads' worth.
-template <typename T, class F>
+// the widest ring: a backward CTA of 512 threads, or a forward one of 512 with two accesses each
+constexpr size_t kNormMaxSmem = norm_ring_bytes(4, 1, 512);
+static_assert(norm_ring_bytes(2, 2, 512) <= kNormMaxSmem && norm_ring_bytes(4, 2, 256) <= kNormMaxSmem, "ring");
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// Call f(V, NV, MAXT, threads, rows per CTA) for rows of d elements of T: 16-byte accesses when d is a
+// multiple of their elements and every row pointer is 16-byte aligned, else one element an
+// access.  A warp per row up to 64 accesses (a CTA of one warp would leave the SM half empty, a
+// wider one waits at barriers); above, per access half a thread (forward) or one (backward,
+// whose column sums take registers), up to 1024 threads.
+template <typename T, bool BWD, class F>
 cudaError_t with_row_shape(int d, bool vec, F&& f) {
-  auto c = [](auto v) { return v; };
-  (void)c;
+  auto threads = [](int n) { return (n + 31) / 32 * 32; };
   if (vec) {
     constexpr int V = 16 / sizeof(T);
-    std::integral_constant<int, V> v;
     const int n = d / V;
-    std::integral_constant<int, 1> one;
-    std::integral_constant<int, 2> two;
-    std::integral_constant<int, 4> four;
-    if (n <= 64) return f(v, one, std::integral_constant<int, 64>{});
-    if (n <= 128) return f(v, one, std::integral_constant<int, 128>{});
-    if (n <= 256) return f(v, two, std::integral_constant<int, 128>{});
-    if (n <= 512) return f(v, two, std::integral_constant<int, 256>{});
-    if (n <= 1024) return f(v, two, std::integral_constant<int, 512>{});
-    if (n <= 2048) return f(v, two, std::integral_constant<int, 1024>{});
-    return f(v, four, std::integral_constant<int, 1024>{});
+    constexpr int NV = BWD ? 1 : 2;
+    if (n <= 32) return f(Int<V>{}, Int<1>{}, Int<32>{}, 32 * kNormWarps, kNormWarps);
+    if (n <= 64) return f(Int<V>{}, Int<2>{}, Int<32>{}, 32 * kNormWarps, kNormWarps);
+    if (n <= NV * 256) return f(Int<V>{}, Int<NV>{}, Int<256>{}, threads((n + NV - 1) / NV), 1);
+    if (n <= NV * 512) return f(Int<V>{}, Int<NV>{}, Int<512>{}, threads((n + NV - 1) / NV), 1);
+    if (BWD && n <= 1024) return f(Int<V>{}, Int<1>{}, Int<1024>{}, threads(n), 1);
+    if (n <= 2048) return f(Int<V>{}, Int<2>{}, Int<1024>{}, threads((n + 1) / 2), 1);
+    return f(Int<V>{}, Int<4>{}, Int<1024>{}, threads((n + 3) / 4), 1);
   }
-  std::integral_constant<int, 1> v;
-  std::integral_constant<int, 8> eight;
-  std::integral_constant<int, 16> sixteen;
-  if (d <= 512) return f(v, eight, std::integral_constant<int, 64>{});
-  if (d <= 1024) return f(v, eight, std::integral_constant<int, 128>{});
-  if (d <= 4096) return f(v, eight, std::integral_constant<int, 512>{});
-  if (d <= 8192) return f(v, eight, std::integral_constant<int, 1024>{});
-  return f(v, sixteen, std::integral_constant<int, 1024>{});
+  if (d <= 256) return f(Int<1>{}, Int<8>{}, Int<32>{}, 32 * kNormWarps, kNormWarps);
+  if (d <= 2048) return f(Int<1>{}, Int<8>{}, Int<256>{}, threads((d + 7) / 8), 1);
+  if (d <= 4096) return f(Int<1>{}, Int<8>{}, Int<512>{}, threads((d + 7) / 8), 1);
+  if (d <= 8192) return f(Int<1>{}, Int<8>{}, Int<1024>{}, threads((d + 7) / 8), 1);
+  return f(Int<1>{}, Int<16>{}, Int<1024>{}, threads((d + 15) / 16), 1);
 }
 
-int norm_parts(int64_t T) { return T < kNormMaxParts ? (int)T : kNormMaxParts; }
+// CTAs of a persistent kernel: as many as are resident at once (asked for once per device and
+// CTA size, which also raises the kernel's shared-memory limit), at most one per row (or eight).
+struct NormOccupancy {
+  std::atomic<int> per_sm[64][33];
+};
+cudaError_t norm_grid(const void* kernel, NormOccupancy& kept, int device, int threads, size_t smem,
+                      int rows_per_cta, int64_t T, int n_sms, int* grid) {
+  std::atomic<int>* known = device < 64 ? &kept.per_sm[device][threads / 32] : nullptr;
+  int per_sm = known ? known->load(std::memory_order_acquire) : 0;
+  if (per_sm == 0) {
+    // the widest CTA's need: the limit is the kernel's, whatever this call's size
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormMaxSmem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) per_sm = 1;
+    if (known) known->store(per_sm, std::memory_order_release);
+  }
+  int64_t g = (T + rows_per_cta - 1) / rows_per_cta;
+  if (g > (int64_t)n_sms * per_sm) g = (int64_t)n_sms * per_sm;
+  *grid = (int)g;
+  return cudaSuccess;
+}
+
+int norm_max_parts(int64_t T) { return T < kNormMaxParts ? (int)T : kNormMaxParts; }
 
 moe_status check_shape(int64_t T, int32_t d, int32_t dtype, int32_t gate_kind, const float* gate,
                        const void* y, const float* w_post, const float* w_pre, float beta) {
@@ -73,16 +97,28 @@ bool rows_vec(int32_t d, int es, std::initializer_list<const void*> rows,
 }
 
 template <typename T>
-cudaError_t launch_fwd(const BlockNormArgs& a, bool vec, cudaStream_t st) {
-  return with_row_shape<T>(a.d, vec, [&](auto v, auto nv, auto tpr) {
-    return launch_pdl(block_norm_kernel<T, v(), nv(), tpr()>, dim3((unsigned)a.T), dim3(tpr()), 0, st, a);
+cudaError_t launch_fwd(const BlockNormArgs& a, bool vec, int device, int n_sms, cudaStream_t st) {
+  return with_row_shape<T, false>(a.d, vec, [&](auto v, auto nv, auto maxt, int threads, int rows) {
+    static NormOccupancy kept;
+    auto kernel = block_norm_kernel<T, v(), nv(), maxt()>;
+    const size_t smem = norm_rings(v(), maxt()) ? norm_ring_bytes(2, nv(), threads) : 0;
+    int grid = 0;
+    const cudaError_t e = norm_grid((const void*)kernel, kept, device, threads, smem, rows, a.T, n_sms, &grid);
+    return e != cudaSuccess ? e : launch_pdl(kernel, dim3(grid), dim3(threads), smem, st, a);
   });
 }
 
+// *parts: the CTAs, each with its own partial sums.
 template <typename T>
-cudaError_t launch_bwd(const BlockNormBwdArgs& a, int parts, bool vec, cudaStream_t st) {
-  return with_row_shape<T>(a.d, vec, [&](auto v, auto nv, auto tpr) {
-    return launch_pdl(block_norm_bwd_kernel<T, v(), nv(), tpr()>, dim3(parts), dim3(tpr()), 0, st, a);
+cudaError_t launch_bwd(const BlockNormBwdArgs& a, bool vec, int device, int n_sms, int* parts, cudaStream_t st) {
+  return with_row_shape<T, true>(a.d, vec, [&](auto v, auto nv, auto maxt, int threads, int rows) {
+    static NormOccupancy kept;
+    auto kernel = block_norm_bwd_kernel<T, v(), nv(), maxt()>;
+    const size_t smem = norm_rings(v(), maxt()) ? norm_ring_bytes(4, nv(), threads) : 0;
+    const cudaError_t e = norm_grid((const void*)kernel, kept, device, threads, smem, rows, a.T, n_sms, parts);
+    if (e != cudaSuccess) return e;
+    if (*parts > kNormMaxParts) *parts = kNormMaxParts;
+    return launch_pdl(kernel, dim3(*parts), dim3(threads), smem, st, a);
   });
 }
 
@@ -111,19 +147,20 @@ moe_status moe_block_norm(const void* x, const void* y, const float* gate, int32
     for (const void* i : {x, y})
       if (o != i && overlaps(o, bytes, i, bytes))
         return fail(MOE_ERR_INVALID_ARG, "an output overlaps an input without being the same buffer");
-  int n_sms = 0;
-  MOE_TRY(op_device(&n_sms));
+  int n_sms = 0, device = 0;
+  MOE_TRY(op_device(&n_sms, &device));
   BlockNormArgs a{x, y, gate, post_weight, pre_weight, r, u, post_rstd, pre_rstd, T, d, gate_kind, beta, eps};
   const bool vec = rows_vec(d, es, {x, y, r, u},
                             {post_weight, pre_weight, gate_kind == kGateChannel ? gate : nullptr});
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  MOE_CUDA(dtype == MOE_BF16 ? launch_fwd<__nv_bfloat16>(a, vec, st) : launch_fwd<float>(a, vec, st));
+  MOE_CUDA((dtype == MOE_BF16 ? launch_fwd<__nv_bfloat16>(a, vec, device, n_sms, st)
+                              : launch_fwd<float>(a, vec, device, n_sms, st)));
   return MOE_OK;
 }
 
 size_t moe_block_norm_workspace(int64_t T, int32_t d) {
   if (T < 1 || d < 1 || d > kNormMaxD) return 0;
-  return (size_t)norm_parts(T) * d * 2 * sizeof(float);
+  return (size_t)norm_max_parts(T) * d * 2 * sizeof(float);
 }
 
 moe_status moe_block_norm_backward(const void* y, const void* r, const void* dr, const void* du,
@@ -159,19 +196,19 @@ moe_status moe_block_norm_backward(const void* y, const void* r, const void* dr,
         return fail(MOE_ERR_INVALID_ARG, "an output overlaps an input without being the same buffer");
   if (!workspace || !aligned16(workspace) || workspace_bytes < moe_block_norm_workspace(T, d))
     return fail(MOE_ERR_INVALID_ARG, "workspace must be 16-byte aligned and hold moe_block_norm_workspace bytes");
-  int n_sms = 0;
-  MOE_TRY(op_device(&n_sms));
+  int n_sms = 0, device = 0;
+  MOE_TRY(op_device(&n_sms, &device));
   const bool need_s = post_weight || channel;
-  const int parts = norm_parts(T);
+  int parts = 0;
   float* part = static_cast<float*>(workspace);
   float* part_pre = pre_weight ? part : nullptr;
-  float* part_s = need_s ? part + (size_t)parts * d : nullptr;
+  float* part_s = need_s ? part + (size_t)norm_max_parts(T) * d : nullptr;
   BlockNormBwdArgs a{y, r, dr, du, gate, post_weight, pre_weight, post_rstd, pre_rstd, dx, dy,
                      gate_kind == kGateToken ? d_gate : nullptr, part_pre, part_s, T, d, gate_kind, beta};
   const bool vec = rows_vec(d, es, {y, r, dr, du, dx, dy},
                             {post_weight, pre_weight, channel ? gate : nullptr});
-  MOE_CUDA((dtype == MOE_BF16 ? launch_bwd<__nv_bfloat16>(a, parts, vec, st)
-                              : launch_bwd<float>(a, parts, vec, st)));
+  MOE_CUDA((dtype == MOE_BF16 ? launch_bwd<__nv_bfloat16>(a, vec, device, n_sms, &parts, st)
+                              : launch_bwd<float>(a, vec, device, n_sms, &parts, st)));
   if (part_pre || part_s) {
     NormReduceArgs ra{part_pre, part_s, parts, d, post_weight, channel ? gate : nullptr, d_pre_weight,
                       d_post_weight, channel ? d_gate : nullptr};
