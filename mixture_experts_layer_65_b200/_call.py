@@ -11,9 +11,9 @@ DTYPES = {torch.bfloat16: _lib.MOE_BF16, torch.float32: _lib.MOE_FP32}
 
 def check_tensor(name: str, t, device, shape: tuple, dtype) -> None:
     """`t` must be a contiguous CUDA tensor on `device` of the given shape and dtype."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
 
 
@@ -24,6 +24,11 @@ def rows_of(name: str, t) -> tuple:
     if t.dim() != 2 or t.dtype not in DTYPES or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [rows, width] torch.bfloat16 or torch.float32 tensor")
     return t.device, t.shape[0], t.shape[1], t.dtype
+
+
+# the current stream's handle without a Stream object around it, where torch has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class on_stream:
@@ -38,11 +43,10 @@ class on_stream:
 
     def __enter__(self) -> int:
         if self.stream is None:
-            current = torch.cuda.current_stream(self.device)
             if torch.cuda.current_device() != self.device.index:
                 self.ctx = torch.cuda.device(self.device)
                 self.ctx.__enter__()
-            return current.cuda_stream
+            return _raw_stream(self.device.index)
         if self.stream.device != self.device:
             raise ValueError(f"stream is on {self.stream.device}, the tensors are on {self.device}")
         if self.stream != torch.cuda.current_stream(self.device):

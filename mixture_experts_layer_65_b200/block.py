@@ -84,7 +84,7 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, gate: torch.Te
         elif y is None:
             out = out._replace(r=x)
         check(lib().moe_block_norm(_ptr(x), _ptr(y), _ptr(gate), kind, _ptr(post_weight), _ptr(pre_weight),
-                                   rows, d, DTYPES[dt], float(beta), float(eps),
+                                   rows, d, DTYPES[dt], beta, eps,
                                    _ptr(out.r) if y is not None else None, _ptr(out.u),
                                    _ptr(out.post_rstd), _ptr(out.pre_rstd), s))
     return out
@@ -115,16 +115,17 @@ def block_norm_backward(fwd: BlockNorm, y: torch.Tensor | None, *, dr: torch.Ten
         g = BlockNormGrads(
             dx=torch.empty_like(fwd.r), dy=torch.empty_like(fwd.r) if y is not None else None,
             d_gate=torch.empty_like(gate) if gate is not None else None,
-            d_post_weight=torch.empty(d, dtype=torch.float32, device=dev) if post_weight is not None else None,
-            d_pre_weight=torch.empty(d, dtype=torch.float32, device=dev) if pre_weight is not None else None)
-        size = lib().moe_block_norm_workspace(rows, d)
+            d_post_weight=torch.empty_like(post_weight) if post_weight is not None else None,
+            d_pre_weight=torch.empty_like(pre_weight) if pre_weight is not None else None)
+        L = lib()
+        size = L.moe_block_norm_workspace(rows, d)
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
-        check(lib().moe_block_norm_backward(
-            _ptr(y), _ptr(fwd.r), _ptr(dr), _ptr(du), _ptr(gate), kind, _ptr(post_weight), _ptr(pre_weight),
-            _ptr(fwd.post_rstd) if post_weight is not None else None,
-            _ptr(fwd.pre_rstd) if pre_weight is not None else None, rows, d, DTYPES[dt], float(beta),
-            _ptr(g.dx), _ptr(g.dy), _ptr(g.d_gate), _ptr(g.d_post_weight), _ptr(g.d_pre_weight),
-            _ptr(ws), size, s))
+        check(L.moe_block_norm_backward(
+            _ptr(y), fwd.r.data_ptr(), _ptr(dr), _ptr(du), _ptr(gate), kind, _ptr(post_weight), _ptr(pre_weight),
+            fwd.post_rstd.data_ptr() if post_weight is not None else None,
+            fwd.pre_rstd.data_ptr() if pre_weight is not None else None, rows, d, DTYPES[dt], beta,
+            g.dx.data_ptr(), _ptr(g.dy), _ptr(g.d_gate), _ptr(g.d_post_weight), _ptr(g.d_pre_weight),
+            ws.data_ptr(), size, s))
     return g
 
 
