@@ -309,8 +309,10 @@ void moe_ep_destroy(moe_ep_handle* handle);
  * the last expert's are not read into any result and not written; a negative count counts as
  * 0, and rows that counts claims past `rows` are ignored.  1 <= n_groups <= 1024, rows < 2^30
  * (0 allowed), any n and k up to 2^20; bf16 products with n and k multiples of 8 and 16-byte
- * aligned buffers run on the tensor cores, others on the CUDA cores.  An output may not
- * overlap an input.  No workspace, no allocation, no host synchronisation; deterministic.
+ * aligned buffers are read by TMA, other bf16 ones element by element.  An output may not
+ * overlap an input.  workspace: moe_grouped_wgrad_workspace bytes of 16-byte aligned DEVICE memory
+ * (0, then NULL, unless a weight gradient with few tiles and many rows is split over its rows),
+ * free again when the call's work is done.  No allocation, no host synchronisation; deterministic.
  * Each result depends only on its own expert's rows (infinities and NaNs of other rows do
  * not reach it).  */
 moe_status moe_grouped_mm(const void* x, const void* w, const int32_t* counts, int32_t n_groups,
@@ -321,7 +323,9 @@ moe_status moe_grouped_mm_dgrad(const void* dy, const void* w, const int32_t* co
                                 void* dx, moe_stream_t stream);
 moe_status moe_grouped_mm_wgrad(const void* dy, const void* x, const int32_t* counts,
                                 int32_t n_groups, int64_t rows, int32_t n, int32_t k, int32_t dtype,
-                                int32_t accumulate, float* dw, moe_stream_t stream);
+                                int32_t accumulate, float* dw, void* workspace,
+                                size_t workspace_bytes, moe_stream_t stream);
+size_t moe_grouped_wgrad_workspace(int32_t n_groups, int64_t rows, int32_t n, int32_t k, int32_t dtype);
 
 /* Synchronise `stream`, then read and clear the current device's error word of the grouped
  * products: MOE_ERR_DEVICE_CHECK if a kernel of an earlier call (on any stream) recorded an

@@ -69,7 +69,9 @@ _SIGS = {
                                            _P, _P]),
     "moe_grouped_mm": (ctypes.c_int, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _P, _P]),
     "moe_grouped_mm_dgrad": (ctypes.c_int, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _P, _P]),
-    "moe_grouped_mm_wgrad": (ctypes.c_int, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _I32, _P, _P]),
+    "moe_grouped_mm_wgrad": (ctypes.c_int, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _I32, _P, _P,
+                                            ctypes.c_size_t, _P]),
+    "moe_grouped_wgrad_workspace": (ctypes.c_size_t, [_I32, _I64, _I32, _I32, _I32]),
     "moe_grouped_device_status": (ctypes.c_int, [_P]),
     "moe_block_norm": (ctypes.c_int, [_P, _P, _P, _I32, _P, _P, _I64, _I32, _I32, ctypes.c_float,
                                       ctypes.c_float, _P, _P, _P, _P, _P]),

@@ -5,8 +5,12 @@
 //   dgrad:  dx[r, :] = dy[r, :] W_e         dy [rows, N], dx [rows, K]
 //   wgrad:  dW_e     = dy_e^T x_e           dW [G, N, K] fp32, the sum over the expert's rows
 // counts stays on the device (a router writes it): each CTA scans it in its prologue, so a
-// product is one launch and needs no workspace.  Rows behind the last expert's are neither
-// read into a result nor written.
+// product is one launch.  Rows behind the last expert's are neither read into a result nor
+// written.
+//
+// A weight gradient with fewer tiles than the GPU has room for, and long sums, is split: each
+// expert's rows in `splits` parts, each part a gradient of its own in the workspace, added up in
+// order by a second kernel.
 #pragma once
 
 #include "ptx.cuh"
@@ -100,12 +104,53 @@ __device__ __forceinline__ int group_of(const GroupTable& t, int G, int tile) {
   return lo;
 }
 
+// Parts of each expert's rows in a weight gradient of `tiles` tiles whose kernel has room for
+// `slots`: as many as fit, of at least `least` rows on average, 256 at most.
+__host__ __device__ constexpr int wgrad_splits(int64_t rows, int G, int64_t tiles, int slots, int least) {
+  const int64_t fill = slots / tiles, rest = rows / G / least;
+  const int64_t s = fill < rest ? fill : rest;
+  return s < 1 ? 1 : s > 256 ? 256 : (int)s;
+}
+// Part s of an expert's rows: whole MMA steps of 16 rows but for the last part.
+__device__ __forceinline__ void split_rows(int& row0, int& rows, int splits, int s) {
+  const int per = ((rows + splits - 1) / splits + 15) & ~15;
+  const int lo = s * per < rows ? s * per : rows;
+  rows = rows - lo < per ? rows - lo : per;
+  row0 += lo;
+}
+
+// dst[i] (+)= sum over the parts, in order.  V elements a thread and step.
+template <int V>
+__global__ void __launch_bounds__(256) wgrad_sum_kernel(const float* part, int splits, int64_t n, int accumulate,
+                                                        float* dst) {
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V; i < n; i += (int64_t)gridDim.x * 256 * V) {
+    float v[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = 0.f;
+    for (int s = 0; s < splits; ++s) {
+      const float* p = part + (int64_t)s * n + i;
+      if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      } else {
+        v[0] += *p;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) dst[i + j] = accumulate ? dst[i + j] + v[j] : v[j];
+  }
+}
+
 // ------------------------------------------------------------------------ CUDA cores
 // fp32 operands: fp32 FMA (two per instruction) on BM x BN tiles, a thread R x R outputs, 16-deep
 // steps through two buffers in shared memory (the next step's elements are on their way in
 // registers while this one is computed).  V elements a load: 4 when the widths are multiples of 4
-// and the buffers 16-byte aligned, else 1.
+// and the buffers 16-byte aligned, else 1.  Sums are cut into pieces of kGsChunk steps, added up
+// apart: one chain of 4096 additions is off by 1e-6 of the result, pieces by a third of that.
 constexpr int kGsBK = 16;
+constexpr int kGsChunk = 16;   // steps: 256 products
 
 struct GroupedSimtArgs {
   const void* a;        // mm: x, dgrad: dy, wgrad: dy
@@ -114,6 +159,7 @@ struct GroupedSimtArgs {
   void* out;
   int G, rows, N, K;    // of the layer: W is [G, N, K]
   int accumulate;       // wgrad: add to out
+  int splits;           // wgrad: parts of the rows, each with its own [G, N, K] in out
 };
 
 // Two fp32 fused multiply-adds, each rounded to nearest.
@@ -143,15 +189,20 @@ __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(Grouped
   const int out_cols = OP == kGroupedMM ? p.N : p.K;
   const int nt = (out_cols + BN - 1) / BN;
   const int mt_w = (p.N + BM - 1) / BM;   // row tiles of a weight gradient
-  group_table(tab, p.counts, p.G, p.rows, W ? 0 : BM, W ? nt * mt_w : nt);
+  group_table(tab, p.counts, p.G, p.rows, W ? 0 : BM, W ? nt * mt_w * p.splits : nt);
   const int total = tab.tile0[p.G];
   const int tid = threadIdx.x, tx = tid % (BN / R), ty = tid / (BN / R);
   const int lda = OP == kGroupedMM ? p.K : p.N;
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
     const int g = group_of(tab, p.G, tile);
-    const int local = tile - tab.tile0[g];
+    int local = tile - tab.tile0[g], part = 0;
+    int grow0 = tab.row0[g], grows = tab.row0[g + 1] - grow0;
+    if constexpr (W) {
+      part = local / (nt * mt_w);
+      local -= part * (nt * mt_w);
+      split_rows(grow0, grows, p.splits, part);
+    }
     const int m0 = local / nt * BM, n0 = (local - local / nt * nt) * BN;
-    const int grow0 = tab.row0[g], grows = tab.row0[g + 1] - grow0;
     const int M = W ? p.N : grows;
     const int Q = OP == kGroupedMM ? p.K : OP == kGroupedDgrad ? p.N : grows;
     const float* A = static_cast<const float*>(p.a) + (size_t)grow0 * lda;
@@ -199,18 +250,18 @@ __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(Grouped
       }
     };
     // a thread's outputs: R / 4 runs of four rows (columns), BM / (R / 4) (BN / (R / 4)) apart
-    float2 acc[R][R / 2];
+    float2 acc[R][R / 2], sum[R][R / 2];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int j = 0; j < R / 2; ++j) acc[i][j] = make_float2(0.f, 0.f);
+      for (int j = 0; j < R / 2; ++j) acc[i][j] = sum[i][j] = make_float2(0.f, 0.f);
     constexpr int kRunM = BM / (R / 4), kRunN = BN / (R / 4);
     if (Q > 0) {
       fetch(0);
       __syncthreads();   // the previous tile's last step has been read
       put(0);
       __syncthreads();
-      int buf = 0;
+      int buf = 0, steps = 0;
       for (int q0 = 0; q0 < Q; q0 += kGsBK, buf ^= 1) {
         const bool more = q0 + kGsBK < Q;
         if (more) fetch(q0 + kGsBK);
@@ -228,6 +279,17 @@ __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(Grouped
 #pragma unroll
             for (int j = 0; j < R / 2; ++j) acc[i][j] = fma2(make_float2(av[i], av[i]), bv[j], acc[i][j]);
         }
+        if (++steps == kGsChunk) {
+          steps = 0;
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < R / 2; ++j) {
+              sum[i][j].x += acc[i][j].x;
+              sum[i][j].y += acc[i][j].y;
+              acc[i][j] = make_float2(0.f, 0.f);
+            }
+        }
         if (more) {
           put(buf ^ 1);
           __syncthreads();
@@ -242,10 +304,10 @@ __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(Grouped
       for (int j = 0; j < R; ++j) {
         const int n = n0 + j / 4 * kRunN + tx * 4 + j % 4;
         if (n >= out_cols) continue;
-        const float v = j & 1 ? acc[i][j / 2].y : acc[i][j / 2].x;
+        const float v = j & 1 ? sum[i][j / 2].y + acc[i][j / 2].y : sum[i][j / 2].x + acc[i][j / 2].x;
         if constexpr (W) {
           if (Q == 0 && p.accumulate) continue;   // nothing to add: not touched
-          float* o = static_cast<float*>(p.out) + ((size_t)g * p.N + m) * p.K + n;
+          float* o = static_cast<float*>(p.out) + (((size_t)part * p.G + g) * p.N + m) * p.K + n;
           *o = p.accumulate ? *o + v : v;
         } else {
           static_cast<float*>(p.out)[(size_t)(grow0 + m) * out_cols + n] = v;

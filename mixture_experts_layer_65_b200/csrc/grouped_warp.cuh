@@ -24,6 +24,7 @@ struct GroupedWarpArgs {
   void* out;
   int G, rows, N, K;        // of the layer: W is [G, N, K]
   int accumulate;           // wgrad: add to out
+  int splits;               // wgrad: parts of the rows, each with its own [G, N, K] in out
 };
 
 template <bool TRANS>
@@ -72,16 +73,21 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 32, MINB) grouped_warp
   const int out_cols = OP == kGroupedMM ? p.N : p.K;
   const int nt = (out_cols + BN - 1) / BN;
   const int mt_w = (p.N + BM - 1) / BM;   // row tiles of a weight gradient
-  group_table(tab, p.counts, p.G, p.rows, W ? 0 : BM, W ? nt * mt_w : nt);
+  group_table(tab, p.counts, p.G, p.rows, W ? 0 : BM, W ? nt * mt_w * p.splits : nt);
   const int total = tab.tile0[p.G];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wm = warp % (BM / WM) * WM, wn = warp / (BM / WM) * WN;
   const int lda = OP == kGroupedMM ? p.K : p.N;
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
     const int g = group_of(tab, p.G, tile);
-    const int local = tile - tab.tile0[g];
+    int local = tile - tab.tile0[g], part = 0;
+    int grow0 = tab.row0[g], grows = tab.row0[g + 1] - grow0;
+    if constexpr (W) {
+      part = local / (nt * mt_w);
+      local -= part * (nt * mt_w);
+      split_rows(grow0, grows, p.splits, part);
+    }
     const int m0 = local / nt * BM, n0 = (local - local / nt * nt) * BN;
-    const int grow0 = tab.row0[g], grows = tab.row0[g + 1] - grow0;
     const int M = W ? p.N : grows;
     const int Q = OP == kGroupedMM ? p.K : OP == kGroupedDgrad ? p.N : grows;
     const __nv_bfloat16* A = p.a + (size_t)grow0 * lda;
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 32, MINB) grouped_warp
           if (m >= M || n >= out_cols) continue;
           if constexpr (W) {
             if (Q == 0 && p.accumulate) continue;   // nothing to add: not touched
-            float* o = static_cast<float*>(p.out) + ((size_t)g * p.N + m) * p.K + n;
+            float* o = static_cast<float*>(p.out) + (((size_t)part * p.G + g) * p.N + m) * p.K + n;
             const float v = sum[i][j][x] + acc[i][j][x];
             *o = p.accumulate ? *o + v : v;
           } else {

@@ -56,6 +56,7 @@ struct GroupedWgradArgs {
   const int32_t* counts;
   int G, rows, N, K;     // dW is [G, N, K]
   int accumulate;        // add to dW
+  int splits;            // parts of the rows, each with its own [G, N, K]
 };
 
 // The experts' first rows, and the experts in order of falling row counts.
@@ -197,18 +198,22 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   __syncthreads();
 
   struct Tile {
-    int g, m, n;      // expert, 256-row block, 256-column block of dW_g
-    int row0, grows;  // the expert's rows
+    int z, m, n;      // part times G plus expert; 256-row block, 256-column block of dW
+    int row0, grows;  // the expert's rows of this part
     int kb;           // stages
   };
   auto tile_of = [&](int tile) {
     Tile c;
-    const int o = tile / per_group, local = tile - o * per_group;
-    c.g = tab.order[o];
+    const int o = tile / (per_group * a.splits);
+    int local = tile - o * (per_group * a.splits);
+    const int part = local / per_group, g = tab.order[o];
+    local -= part * per_group;
+    c.z = part * a.G + g;
     c.m = local / nt;
     c.n = local - c.m * nt;
-    c.row0 = tab.row0[c.g];
-    c.grows = tab.row0[c.g + 1] - c.row0;
+    c.row0 = tab.row0[g];
+    c.grows = tab.row0[g + 1] - c.row0;
+    split_rows(c.row0, c.grows, a.splits, part);
     c.kb = (c.grows + kGwRows - 1) / kGwRows;
     return c;
   };
@@ -452,7 +457,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(&tmOut, smem_u32(stage_out), col0 + x * kGwStoreCols, mrow0, c.g, a.accumulate);
+            tma_store_3d(&tmOut, smem_u32(stage_out), col0 + x * kGwStoreCols, mrow0, c.z, a.accumulate);
             bulk_commit();
           }
         }

@@ -48,17 +48,17 @@ int64_t tiles_of(const Shape& s, int bm, int bn) {
 template <int OP, int BM, int BN, int R, int V>
 cudaError_t launch_simt_tile(const GroupedSimtArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
   constexpr int kThreads = BM * BN / (R * R);
-  const int64_t tiles = tiles_of<OP>(s, BM, BN), most = (int64_t)n_sms * (1024 / kThreads);
+  const int64_t tiles = a.splits * tiles_of<OP>(s, BM, BN), most = (int64_t)n_sms * (1024 / kThreads);
   return launch_pdl(grouped_simt_kernel<OP, BM, BN, R, V>, dim3((unsigned)(tiles < most ? tiles : most)),
                     dim3(kThreads), 0, st, a);
 }
 template <int OP>
 cudaError_t launch_simt(const GroupedSimtArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
   const bool v4 = s.n % 4 == 0 && s.k % 4 == 0 && aligned16(a.a) && aligned16(a.b);
-  if (tiles_of<OP>(s, 128, 128) >= 2 * n_sms)
+  if (a.splits * tiles_of<OP>(s, 128, 128) >= 2 * n_sms)
     return v4 ? launch_simt_tile<OP, 128, 128, 8, 4>(a, s, n_sms, st)
               : launch_simt_tile<OP, 128, 128, 8, 1>(a, s, n_sms, st);
-  if (tiles_of<OP>(s, 64, 64) >= 3 * n_sms)
+  if (a.splits * tiles_of<OP>(s, 64, 64) >= 3 * n_sms)
     return v4 ? launch_simt_tile<OP, 64, 64, 8, 4>(a, s, n_sms, st)
               : launch_simt_tile<OP, 64, 64, 8, 1>(a, s, n_sms, st);
   return launch_simt_tile<OP, 32, 32, 4, 1>(a, s, n_sms, st);
@@ -68,13 +68,13 @@ cudaError_t launch_simt(const GroupedSimtArgs& a, const Shape& s, int n_sms, cud
 template <int OP, int BM, int BN, int WM, int WN>
 cudaError_t launch_warp_tile(const GroupedWarpArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
   constexpr int kThreads = (BM / WM) * (BN / WN) * 32;
-  const int64_t tiles = tiles_of<OP>(s, BM, BN), most = (int64_t)n_sms * (512 / kThreads);
+  const int64_t tiles = a.splits * tiles_of<OP>(s, BM, BN), most = (int64_t)n_sms * (512 / kThreads);
   return launch_pdl(grouped_warp_kernel<OP, BM, BN, WM, WN, 512 / kThreads>, dim3((unsigned)(tiles < most ? tiles : most)),
                     dim3(kThreads), 0, st, a);
 }
 template <int OP>
 cudaError_t launch_warp(const GroupedWarpArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
-  if (tiles_of<OP>(s, 128, 128) >= n_sms) return launch_warp_tile<OP, 128, 128, 64, 32>(a, s, n_sms, st);
+  if (a.splits * tiles_of<OP>(s, 128, 128) >= n_sms) return launch_warp_tile<OP, 128, 128, 64, 32>(a, s, n_sms, st);
   return launch_warp_tile<OP, 64, 64, 32, 32>(a, s, n_sms, st);
 }
 
@@ -120,19 +120,19 @@ bool encode_out_f32(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t ou
 // The products on the tensor cores: bf16, widths in whole 16-byte vectors, aligned buffers.
 template <int OP>
 moe_status launch_tc(const void* a, const void* b, const int32_t* counts, const Shape& s, int accumulate,
-                     void* out, int device, int n_sms, cudaStream_t st) {
+                     int splits, void* out, int device, int n_sms, cudaStream_t st) {
   static std::atomic<int> kept[64];
   CUtensorMap tmA, tmB;
   int clusters = 0;
   if constexpr (OP == kGroupedWgrad) {
     CUtensorMap tmOut;
     if (!encode_2d(&tmA, a, s.n, s.rows, kGwRows) || !encode_2d(&tmB, b, s.k, s.rows, kGwRows) ||
-        !encode_out_f32(&tmOut, out, s.k, s.n, s.G))
+        !encode_out_f32(&tmOut, out, s.k, s.n, (uint64_t)splits * s.G))
       return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for a grouped product's operand");
     MOE_TRY(pair_clusters((const void*)grouped_wgrad_kernel, kGwThreads, kGwSmemBytes, kept, device, n_sms, &clusters));
     // a cluster per tile
-    const int64_t tiles = (int64_t)s.G * ((s.n + kPairBM - 1) / kPairBM) * ((s.k + kGemmBN - 1) / kGemmBN);
-    GroupedWgradArgs p{counts, s.G, (int)s.rows, s.n, s.k, accumulate};
+    const int64_t tiles = splits * tiles_of<OP>(s, kPairBM, kGemmBN);
+    GroupedWgradArgs p{counts, s.G, (int)s.rows, s.n, s.k, accumulate, splits};
     MOE_CUDA(launch_pdl(grouped_wgrad_kernel, dim3(2 * (unsigned)tiles), dim3(kGwThreads), kGwSmemBytes, st, tmA,
                         tmB, tmOut, p));
   } else {
@@ -152,9 +152,22 @@ moe_status launch_tc(const void* a, const void* b, const int32_t* counts, const 
   return MOE_OK;
 }
 
+bool takes_tma(const Shape& s, const void* a, const void* b, const void* out) {
+  return s.dtype == MOE_BF16 && s.n % 8 == 0 && s.k % 8 == 0 && s.rows > 0 && aligned16(a) && aligned16(b) &&
+         aligned16(out);
+}
+
+// Parts of a weight gradient's rows: by the tiles of the kernel that runs it.  (Slots and tile
+// sizes are those of a B200's 148 SMs, so that the workspace's size needs no device.)
+int splits_of(const Shape& s, bool tma) {
+  constexpr int kSms = 148;
+  if (tma) return wgrad_splits(s.rows, s.G, tiles_of<kGroupedWgrad>(s, kPairBM, kGemmBN), kSms / 2, 1024);
+  return wgrad_splits(s.rows, s.G, tiles_of<kGroupedWgrad>(s, 64, 64), 4 * kSms, 512);
+}
+
 template <int OP>
 moe_status product(const void* a, const void* b, const int32_t* counts, const Shape& s, int accumulate,
-                   void* out, moe_stream_t stream) {
+                   void* out, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   MOE_TRY(check_shape(s));
   constexpr bool W = OP == kGroupedWgrad;
   const size_t es = s.dtype == MOE_BF16 ? 2 : 4;
@@ -170,19 +183,39 @@ moe_status product(const void* a, const void* b, const int32_t* counts, const Sh
   if (overlaps(out, o_bytes, a, a_bytes) || overlaps(out, o_bytes, b, b_bytes) ||
       overlaps(out, o_bytes, counts, (size_t)s.G * 4))
     return fail(MOE_ERR_INVALID_ARG, "the output overlaps an input");
+  const bool tma = takes_tma(s, a, b, out);
+  const int splits = W ? splits_of(s, tma) : 1;
+  void* dst = out;   // of the product's kernel
+  if (splits > 1) {
+    const size_t need = splits * o_bytes;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need)
+      return fail(MOE_ERR_INVALID_ARG, "workspace must be 16-byte aligned and hold moe_grouped_wgrad_workspace bytes");
+    if (overlaps(workspace, need, a, a_bytes) || overlaps(workspace, need, b, b_bytes) ||
+        overlaps(workspace, need, out, o_bytes) || overlaps(workspace, need, counts, (size_t)s.G * 4))
+      return fail(MOE_ERR_INVALID_ARG, "the workspace overlaps an input or the output");
+    dst = workspace;
+  }
   int n_sms = 0, device = 0;
   MOE_TRY(op_device(&n_sms, &device));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (s.dtype == MOE_BF16 && s.n % 8 == 0 && s.k % 8 == 0 && s.rows > 0 && aligned16(a) && aligned16(b) &&
-      aligned16(out))
-    return launch_tc<OP>(a, b, counts, s, accumulate, out, device, n_sms, st);
-  if (s.dtype == MOE_BF16) {
-    GroupedWarpArgs p{static_cast<const __nv_bfloat16*>(a), static_cast<const __nv_bfloat16*>(b), counts, out, s.G,
-                      (int)s.rows, s.n, s.k, accumulate};
+  const int add = splits > 1 ? 0 : accumulate;
+  if (tma) {
+    MOE_TRY(launch_tc<OP>(a, b, counts, s, add, splits, dst, device, n_sms, st));
+  } else if (s.dtype == MOE_BF16) {
+    GroupedWarpArgs p{static_cast<const __nv_bfloat16*>(a), static_cast<const __nv_bfloat16*>(b), counts, dst, s.G,
+                      (int)s.rows, s.n, s.k, add, splits};
     MOE_CUDA(launch_warp<OP>(p, s, n_sms, st));
   } else {
-    GroupedSimtArgs p{a, b, counts, out, s.G, (int)s.rows, s.n, s.k, accumulate};
+    GroupedSimtArgs p{a, b, counts, dst, s.G, (int)s.rows, s.n, s.k, add, splits};
     MOE_CUDA(launch_simt<OP>(p, s, n_sms, st));
+  }
+  if (splits > 1) {
+    const int64_t n = (int64_t)s.G * s.n * s.k;
+    const bool v4 = n % 4 == 0 && aligned16(out);
+    int64_t grid = (n / (v4 ? 4 : 1) + 255) / 256;
+    if (grid > 8 * (int64_t)n_sms) grid = 8 * (int64_t)n_sms;
+    MOE_CUDA(launch_pdl(v4 ? wgrad_sum_kernel<4> : wgrad_sum_kernel<1>, dim3((unsigned)grid), dim3(256), 0, st,
+                        static_cast<const float*>(workspace), splits, n, accumulate, static_cast<float*>(out)));
   }
   return MOE_OK;
 }
@@ -193,19 +226,30 @@ extern "C" {
 
 moe_status moe_grouped_mm(const void* x, const void* w, const int32_t* counts, int32_t n_groups, int64_t rows,
                           int32_t n, int32_t k, int32_t dtype, void* y, moe_stream_t stream) {
-  return product<kGroupedMM>(x, w, counts, Shape{n_groups, rows, n, k, dtype}, 0, y, stream);
+  return product<kGroupedMM>(x, w, counts, Shape{n_groups, rows, n, k, dtype}, 0, y, nullptr, 0, stream);
 }
 
 moe_status moe_grouped_mm_dgrad(const void* dy, const void* w, const int32_t* counts, int32_t n_groups,
                                 int64_t rows, int32_t n, int32_t k, int32_t dtype, void* dx,
                                 moe_stream_t stream) {
-  return product<kGroupedDgrad>(dy, w, counts, Shape{n_groups, rows, n, k, dtype}, 0, dx, stream);
+  return product<kGroupedDgrad>(dy, w, counts, Shape{n_groups, rows, n, k, dtype}, 0, dx, nullptr, 0,
+                                stream);
+}
+
+size_t moe_grouped_wgrad_workspace(int32_t n_groups, int64_t rows, int32_t n, int32_t k, int32_t dtype) {
+  const Shape s{n_groups, rows, n, k, dtype};
+  if (check_shape(s) != MOE_OK || rows == 0) return 0;
+  // (whether TMA takes the buffers is not known here: the larger of the two)
+  const int a = splits_of(s, true), b = splits_of(s, false);
+  const int splits = dtype == MOE_FP32 || n % 8 || k % 8 ? b : a > b ? a : b;
+  return splits > 1 ? (size_t)splits * n_groups * n * k * sizeof(float) : 0;
 }
 
 moe_status moe_grouped_mm_wgrad(const void* dy, const void* x, const int32_t* counts, int32_t n_groups,
                                 int64_t rows, int32_t n, int32_t k, int32_t dtype, int32_t accumulate,
-                                float* dw, moe_stream_t stream) {
-  return product<kGroupedWgrad>(dy, x, counts, Shape{n_groups, rows, n, k, dtype}, accumulate, dw, stream);
+                                float* dw, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  return product<kGroupedWgrad>(dy, x, counts, Shape{n_groups, rows, n, k, dtype}, accumulate, dw, workspace,
+                                workspace_bytes, stream);
 }
 
 moe_status moe_grouped_device_status(moe_stream_t stream) {

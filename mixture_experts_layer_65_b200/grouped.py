@@ -85,8 +85,12 @@ def grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor,
     with on_stream(dev, stream, (dy, x, counts, out)) as s:
         if out is None:
             out = torch.empty(g, n, k, dtype=torch.float32, device=dev)
-        check(lib().moe_grouped_mm_wgrad(dy.data_ptr(), x.data_ptr(), counts.data_ptr(), g, rows, n, k,
-                                         DTYPES[dt], int(bool(accumulate)), out.data_ptr(), s))
+        L = lib()
+        size = L.moe_grouped_wgrad_workspace(g, rows, n, k, DTYPES[dt])
+        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+        check(L.moe_grouped_mm_wgrad(dy.data_ptr(), x.data_ptr(), counts.data_ptr(), g, rows, n, k, DTYPES[dt],
+                                     int(bool(accumulate)), out.data_ptr(), ws.data_ptr() if size else None,
+                                     size, s))
     return out
 
 

@@ -4,6 +4,8 @@ import pytest
 import torch
 
 from mixture_experts_layer_65_b200 import build
+from mixture_experts_layer_65_b200._call import DTYPES
+from mixture_experts_layer_65_b200._lib import lib
 from mixture_experts_layer_65_b200.grouped import grouped_mm, grouped_mm_dgrad, grouped_mm_wgrad
 from tests import operators_ref as R
 
@@ -141,6 +143,44 @@ def test_weight_gradients_accumulate(dt, n, k):
     assert bool(((got.double() - ref).abs() <= tol + R.E * ref.abs() + 2 * R.E * tol).all())
     assert torch.equal(got[1], base[1])     # no rows: as it was
     assert torch.equal(grouped_mm_wgrad(dy, x, c, out=base.clone())[1], torch.zeros_like(base[1]))
+
+
+# few tiles and many rows: the rows are split; parts that are empty, ragged, one expert with all
+SPLIT = {"even": [9000, 9000], "ragged": [20001, 3, 0, 1], "one": [30011]}
+
+
+@pytest.mark.parametrize("counts", SPLIT.values(), ids=SPLIT.keys())
+@pytest.mark.parametrize("dt,n,k", [("bf16", 64, 136), ("bf16", 33, 35), ("fp32", 64, 40), ("fp32", 33, 35)])
+def test_long_weight_gradients_are_split(dt, n, k, counts):
+    dy, x, c = _inputs("wgrad", counts, n, k, DT[dt], tail=3)
+    dy[sum(counts):] = float("nan")
+    assert lib().moe_grouped_wgrad_workspace(len(counts), dy.shape[0], n, k, DTYPES[DT[dt]]) > 0
+    got = grouped_mm_wgrad(dy, x, c)
+    _check("wgrad", dy[:sum(counts)], x[:sum(counts)], c, got)
+    assert torch.equal(grouped_mm_wgrad(dy, x, c), got)
+    base = torch.randn(len(counts), n, k, device="cuda")
+    acc = grouped_mm_wgrad(dy, x, c, out=base.clone(), accumulate=True)
+    assert torch.equal(acc, base + got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = grouped_mm_wgrad(dy, x, c)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again, got)
+
+
+@pytest.mark.parametrize("dt,n,k,q", [("bf16", 64, 64, 100000), ("fp32", 64, 64, 100000), ("bf16", 33, 67, 100000),
+                                      ("fp32", 40, 64, 4096)])
+def test_long_sums_keep_their_precision(dt, n, k, q):
+    """The norm of the error over the norm of the result: below 1e-6, whatever the length of the
+    sum (a single chain of 100,000 fp32 additions, or of truncating ones, is at 1e-5)."""
+    if q == 4096:
+        a, b, c = _inputs("mm", [300], n, q, DT[dt])
+        got, ref = grouped_mm(a, b, c), R.grouped("mm", a, b, c)[0]
+    else:
+        a, b, c = _inputs("wgrad", [q], n, k, DT[dt])
+        got, ref = grouped_mm_wgrad(a, b, c), R.grouped("wgrad", a, b, c)[0]
+    assert float((got.double() - ref).norm() / ref.norm()) < 1e-6
 
 
 @pytest.mark.parametrize("op", ["mm", "dgrad", "wgrad"])

@@ -33,15 +33,30 @@ GROUPED = dict(a=A, b=B, counts=C, g=4, rows=64, n=64, k=64, dtype=_lib.MOE_BF16
 def test_grouped_products_refuse(L, op, kw, status):
     v = {**GROUPED, **kw}
     args = [v["a"], v["b"], v["counts"], v["g"], v["rows"], v["n"], v["k"], v["dtype"]]
-    if op.endswith("wgrad"):
-        args.append(0)
-    assert getattr(L, op)(*args, v["out"], None) == status
+    args += [0, v["out"], None, 0] if op.endswith("wgrad") else [v["out"]]
+    assert getattr(L, op)(*args, None) == status
     assert len(L.moe_last_error()) > 0
 
 
 def test_grouped_products_of_no_rows_do_nothing(L):
     assert L.moe_grouped_mm(None, B, C, 4, 0, 64, 64, _lib.MOE_BF16, None, None) == _lib.MOE_OK
     assert L.moe_grouped_mm_dgrad(None, B, C, 4, 0, 64, 64, _lib.MOE_FP32, None, None) == _lib.MOE_OK
+
+
+def test_split_weight_gradients_want_their_workspace(L):
+    for dt in (_lib.MOE_BF16, _lib.MOE_FP32):
+        assert L.moe_grouped_wgrad_workspace(64, 49152, 1408, 2048, dt) == 0       # tiles enough
+        assert L.moe_grouped_wgrad_workspace(2, 300, 64, 64, dt) == 0              # rows too few
+        size = L.moe_grouped_wgrad_workspace(2, 65536, 64, 64, dt)
+        assert size > 2 * 64 * 64 * 4
+        args = [A, B, C, 2, 65536, 64, 64, dt, 0, D]
+        assert L.moe_grouped_mm_wgrad(*args, None, 0, None) == BAD
+        assert L.moe_grouped_mm_wgrad(*args, D + (1 << 30), 2 * 64 * 64 * 4, None) == BAD   # one part's
+        assert L.moe_grouped_mm_wgrad(*args, D + (1 << 30) + 4, size, None) == BAD
+        assert L.moe_grouped_mm_wgrad(*args, D, size, None) == BAD                 # on the output
+        assert L.moe_grouped_mm_wgrad(*args, A + 64, size, None) == BAD            # on an input
+    assert L.moe_grouped_wgrad_workspace(0, 65536, 64, 64, 1) == 0                 # refused shapes
+    assert L.moe_grouped_wgrad_workspace(2, 0, 64, 64, 1) == 0
 
 
 NORM = dict(x=A, y=B, gate=None, kind=0, post=C, pre=C, T=8, d=64, dtype=_lib.MOE_BF16, beta=1.0, eps=1e-6,
