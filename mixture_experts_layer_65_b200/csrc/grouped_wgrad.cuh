@@ -1,17 +1,22 @@
 // grouped_wgrad.cuh -- the weight gradients of grouped_mm.cuh on the tensor cores (bf16 operands,
 // fp32 result): dW_e = dy_e^T x_e, a product whose contraction runs over the expert's rows.
 //
-// Clusters of two CTAs, 256 x 256 tiles of dW_e, tcgen05.mma with cta_group::2.  dy and x are read
+// Clusters of two CTAs, 256 x 256 tiles of dW_e^T, tcgen05.mma with cta_group::2.  x and dy are read
 // where they lie: their contiguous index is an output index, so both operands are MN-major
-// tiles (boxes of 64 columns x 112 rows).
+// tiles (boxes of 64 columns x 128 rows, one stage of the ring).  The transpose puts dW's
+// contiguous index on the accumulator's lanes: an epilogue warp's store of one accumulator
+// column is a whole 128-byte line, straight from registers (with dW's rows on the lanes, stores of
+// 32 bytes from 32 rows took 2.6 times as long, and TMA stores through shared memory took 32 KB
+// of the ring); and dW's rows, the experts' widths, which are less often multiples of 256 than
+// the model's, are on the MMA's N, whose last tile takes any multiple of 32.
 //
 // Precision: the tensor cores truncate when they add to an accumulator, which over n steps of
 // 16 rows leaves a bias of about 2.2e-8 n of the value (measured: 7.4e-6 of dW's norm when an
-// expert had 10,800 rows in one chain).  So a chain is cut after kGwChunk stages of 112
+// expert had 10,800 rows in one chain).  So a chain is cut after kGwChunk stages of 128
 // rows: the epilogue warps add the pieces in registers with round-to-nearest while the MMA
 // fills the other accumulator.
 //
-// Ragged rows: a tile's last stage runs ceil(t / 16) of its seven MMA steps for t rows, and the
+// Ragged rows: a tile's last stage runs ceil(t / 16) of its eight MMA steps for t rows, and the
 // rows behind t in the last step are zeroed in both operands (0 x NaN would be NaN) by a
 // warp of each CTA before the MMA: that stage's loads complete on a barrier of the CTA, and
 // the leader's zeroing warp, told by the peer's, arrives on the "full" barrier instead of the
@@ -25,36 +30,28 @@
 // the end, and which cluster computes a tile does not change its value.  A warp of each CTA does
 // nothing but ask (the leader's), read the answer and hand the tile on: in the producer that
 // took 2,400 cycles a tile, which the ring could not cover.
-//
-// Output: each epilogue warp passes its 32 rows through shared memory, 32 columns (a box of
-// 128-byte swizzled rows) at a time, to TMA stores, which cut off what lies outside dW.  Plain
-// stores want registers that the sums of a 128-column row leave none of (738 MB of zeros: 255 us
-// against 119); an accumulating call makes them reductions (one addition per element, rounded
-// to nearest; subnormal sums become 0), so nothing is read back.
 #pragma once
 
 #include "grouped_tc.cuh"
 
 namespace moe {
 
-// A stage: 112 rows (seven MMA steps), two boxes of 64 columns each of dy and x; what is left of
-// the shared memory beside three of them holds the output's staging.
-constexpr int kGwRows = 112;
+// A stage: 128 rows (eight MMA steps), two boxes of 64 columns each of x and dy.
+constexpr int kGwRows = 128;
 constexpr int kGwStages = 3;
 constexpr uint32_t kGwBox = kGwRows * 128;
 constexpr uint32_t kGwStageBytes = 4 * kGwBox;
-constexpr int kGwChunk = 4;                                // stages per accumulator chain
+constexpr int kGwChunk = 3;                                // stages per accumulator chain
 constexpr int kGwThreads = 64 + 32 * (kGpEpiWarps + 2);    // + the zeroing and the scheduling warp
 constexpr int kGwSlots = 4;                                // answers, and tiles handed on
 constexpr int kGwAhead = 2;                                // requests made ahead
-constexpr int kGwStoreCols = 32;
-constexpr uint32_t kGwStoreBytes = 32 * kGwStoreCols * 4;  // one epilogue warp's staging
-constexpr size_t kGwSmemBytes = 1024 + kGwStages * kGwStageBytes + 1024 + kGpEpiWarps * kGwStoreBytes;
+constexpr size_t kGwSmemBytes = 1024 + kGwStages * kGwStageBytes + 1024;
 static_assert(kGwBox % 1024 == 0 && kGwRows % 16 == 0, "swizzle atoms, MMA steps");
 
 struct GroupedWgradArgs {
   const int32_t* counts;
-  int G, rows, N, K;     // dW is [G, N, K]
+  float* out;            // [splits, G, N, K]
+  int G, rows, N, K;
   int accumulate;        // add to dW
   int splits;            // parts of the rows, each with its own [G, N, K]
 };
@@ -98,29 +95,9 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_peer(uint32_t cluster_addr
                : "memory");
 }
 
-// Store (or add) a box from shared memory; the part of it outside the tensor is left out.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t c0, int32_t c1,
-                                             int32_t c2, bool add) {
-  if (add)
-    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
-  else
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// All of this thread's stores: their shared memory has been read (and can be written again), or
-// their results are written.
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
 static __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGwThreads, 1)
-grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ CUtensorMap tmOut, GroupedWgradArgs a) {
+grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmDy,
+                     GroupedWgradArgs a) {
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   __shared__ WgradTable tab;
@@ -142,7 +119,6 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   uint64_t* tile_empty = tile_full + kGwSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tile_empty + kGwSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint8_t* store_base = ctl + 1024;   // 1024-byte aligned, as the swizzle wants
   int* err = &g_grouped_err;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -170,9 +146,8 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
-    tma_prefetch_desc(&tmOut);
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmDy);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), kGemmTmemCols);
@@ -183,8 +158,8 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();
-  const int nt = (a.K + kGemmBN - 1) / kGemmBN;                    // column tiles of a gradient
-  const int per_group = nt * ((a.N + kPairBM - 1) / kPairBM);
+  const int nt = (a.N + kGemmBN - 1) / kGemmBN;                    // tiles along a gradient's rows
+  const int per_group = nt * ((a.K + kPairBM - 1) / kPairBM);
   group_rows(tab.row0, a.counts, a.G, a.rows);
   for (int g = threadIdx.x; g < a.G; g += kGwThreads) {
     const int n = tab.row0[g + 1] - tab.row0[g];
@@ -198,7 +173,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   __syncthreads();
 
   struct Tile {
-    int z, m, n;      // part times G plus expert; 256-row block, 256-column block of dW
+    int z, m, n;      // part times G plus expert; 256-column block, 256-row block of dW
     int row0, grows;  // the expert's rows of this part
     int kb;           // stages
   };
@@ -218,7 +193,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     return c;
   };
   auto tile_cols = [&](int n) {   // the MMA's N: a multiple of 32
-    const int left = a.K - n * kGemmBN;
+    const int left = a.N - n * kGemmBN;
     return left >= kGemmBN ? kGemmBN : (left + 31) & ~31;
   };
   auto tail_rows = [&](const Tile& c) { return c.grows - (c.kb - 1) * kGwRows; };   // of the last stage
@@ -260,10 +235,10 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
           if (fix) mbar_arrive_expect_tx(smem_u32(&tail[stage]), kGwStageBytes);
           else if (leader) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2u * kGwStageBytes);
           const int row = c.row0 + kb * kGwRows;
-          tma_load_2d_pair(sa, &tmA, fb, a0, row);
-          tma_load_2d_pair(sa + kGwBox, &tmA, fb, a0 + 64, row);
-          tma_load_2d_pair(sa + 2 * kGwBox, &tmB, fb, b0, row);
-          tma_load_2d_pair(sa + 2 * kGwBox + kGwBox, &tmB, fb, b0 + 64, row);
+          tma_load_2d_pair(sa, &tmX, fb, a0, row);
+          tma_load_2d_pair(sa + kGwBox, &tmX, fb, a0 + 64, row);
+          tma_load_2d_pair(sa + 2 * kGwBox, &tmDy, fb, b0, row);
+          tma_load_2d_pair(sa + 2 * kGwBox + kGwBox, &tmDy, fb, b0 + 64, row);
           if (++stage == kGwStages) { stage = 0; phase ^= 1u; }
         }
         if (ok) tile = next_tile(sl);
@@ -398,12 +373,11 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     // ------------------------------------------------------------------ epilogue
     const int q = warp & 3;                 // TMEM lane quadrant
     const int half = (warp - 2) >> 2;       // which half of the tile's columns
-    uint8_t* stage_out = store_base + (warp - 2) * kGwStoreBytes;
     int it = 0;
     Slot sl;
     for (int tile = first; tile >= 0;) {
       const Tile c = tile_of(tile);
-      // this thread's row of 128 columns; an expert without rows leaves zeros
+      // this thread's column of dW, 128 of its rows; an expert without rows leaves zeros
       uint32_t s[4][32];
       if (c.kb == 0) {
 #pragma unroll
@@ -441,31 +415,23 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         if (lane == 0) mbar_arrive_relaxed_cluster(mapa_shared(smem_u32(&acc_empty[acc]), 0));
       }
       if (!ok) break;
-      const int mrow0 = c.m * kPairBM + (int)rank * 128 + q * 32;   // first of this warp's rows
-      if (mrow0 < a.N && !(c.kb == 0 && a.accumulate)) {
-        const int col0 = c.n * kGemmBN + half * (kGemmBN / 2);
+      const int col = c.m * kPairBM + (int)rank * 128 + q * 32 + lane;
+      const int n0 = c.n * kGemmBN + half * (kGemmBN / 2);
+      if (col < a.K && !(c.kb == 0 && a.accumulate)) {
+        float* o = a.out + ((size_t)c.z * a.N + n0) * a.K + col;
+        const int left = a.N - n0;
 #pragma unroll
-        for (int x = 0; x < kGemmBN / 2 / kGwStoreCols; ++x) {
-          if (col0 + x * kGwStoreCols >= a.K) break;
-          if (lane == 0) bulk_wait_read();
-          __syncwarp();
-          // 16-byte chunk i of this row's 128 bytes at i ^ (row % 8)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(stage_out + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-                make_uint4(s[x][4 * i], s[x][4 * i + 1], s[x][4 * i + 2], s[x][4 * i + 3]);
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&tmOut, smem_u32(stage_out), col0 + x * kGwStoreCols, mrow0, c.z, a.accumulate);
-            bulk_commit();
-          }
+        for (int i = 0; i < kGemmBN / 2; ++i) {
+          if (i % 8 == 0 && i >= left) break;   // (N is a multiple of 8)
+          const float v = __uint_as_float(s[i >> 5][i & 31]);
+          if (a.accumulate) atomicAdd(o, v);    // one addition per element: no order to it
+          else *o = v;
+          o += a.K;
         }
       }
       if (lane == 0) tile = next_tile(sl);
       tile = __shfl_sync(0xffffffffu, tile, 0);
     }
-    if (lane == 0) bulk_wait_all();
   }
 
   // teardown: all MMAs of the pair have completed before TMEM is released in either CTA

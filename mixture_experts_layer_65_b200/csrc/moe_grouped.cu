@@ -103,20 +103,6 @@ moe_status pair_clusters(const void* kernel, int threads, size_t smem, std::atom
   return MOE_OK;
 }
 
-// fp32 [depth, outer, inner], boxes of 32 rows x 32 values (128-byte swizzle): the weight
-// gradients' stores.
-bool encode_out_f32(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t depth) {
-  EncodeTiledFn fn = get_encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {inner, outer, depth};
-  cuuint64_t strides[2] = {inner * 4, inner * outer * 4};
-  cuuint32_t box[3] = {kGwStoreCols, 32, 1};
-  cuuint32_t ess[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(ptr), dims, strides, box, ess,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // The products on the tensor cores: bf16, widths in whole 16-byte vectors, aligned buffers.
 template <int OP>
 moe_status launch_tc(const void* a, const void* b, const int32_t* counts, const Shape& s, int accumulate,
@@ -125,16 +111,14 @@ moe_status launch_tc(const void* a, const void* b, const int32_t* counts, const 
   CUtensorMap tmA, tmB;
   int clusters = 0;
   if constexpr (OP == kGroupedWgrad) {
-    CUtensorMap tmOut;
-    if (!encode_2d(&tmA, a, s.n, s.rows, kGwRows) || !encode_2d(&tmB, b, s.k, s.rows, kGwRows) ||
-        !encode_out_f32(&tmOut, out, s.k, s.n, (uint64_t)splits * s.G))
+    if (!encode_2d(&tmA, a, s.n, s.rows, kGwRows) || !encode_2d(&tmB, b, s.k, s.rows, kGwRows))
       return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for a grouped product's operand");
     MOE_TRY(pair_clusters((const void*)grouped_wgrad_kernel, kGwThreads, kGwSmemBytes, kept, device, n_sms, &clusters));
     // a cluster per tile
     const int64_t tiles = splits * tiles_of<OP>(s, kPairBM, kGemmBN);
-    GroupedWgradArgs p{counts, s.G, (int)s.rows, s.n, s.k, accumulate, splits};
-    MOE_CUDA(launch_pdl(grouped_wgrad_kernel, dim3(2 * (unsigned)tiles), dim3(kGwThreads), kGwSmemBytes, st, tmA,
-                        tmB, tmOut, p));
+    GroupedWgradArgs p{counts, static_cast<float*>(out), s.G, (int)s.rows, s.n, s.k, accumulate, splits};
+    MOE_CUDA(launch_pdl(grouped_wgrad_kernel, dim3(2 * (unsigned)tiles), dim3(kGwThreads), kGwSmemBytes, st, tmB,
+                        tmA, p));
   } else {
     const int rt = gr_tile_rows(s.rows, s.G);
     if (!encode_2d(&tmA, a, OP == kGroupedMM ? s.k : s.n, s.rows, rt / 2) ||
