@@ -140,6 +140,75 @@ __device__ __forceinline__ void store_f32(float* p, const float (&f)[V]) {
   }
 }
 
+// V values at a time, two per instruction where V is even (each product and sum rounded to
+// nearest, as the scalar instructions do).
+__device__ __forceinline__ uint64_t as_pair(float x, float y) {
+  return static_cast<uint64_t>(__float_as_uint(x)) | static_cast<uint64_t>(__float_as_uint(y)) << 32;
+}
+__device__ __forceinline__ void from_pair(uint64_t v, float& x, float& y) {
+  x = __uint_as_float(static_cast<uint32_t>(v));
+  y = __uint_as_float(static_cast<uint32_t>(v >> 32));
+}
+// d = a b + c
+template <int V>
+__device__ __forceinline__ void vfma(float (&d)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      uint64_t v;
+      asm("fma.rn.f32x2 %0, %1, %2, %3;"
+          : "=l"(v)
+          : "l"(as_pair(a[j], a[j + 1])), "l"(as_pair(b[j], b[j + 1])), "l"(as_pair(c[j], c[j + 1])));
+      from_pair(v, d[j], d[j + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] = fmaf(a[j], b[j], c[j]);
+  }
+}
+// d = a b
+template <int V>
+__device__ __forceinline__ void vmul(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      uint64_t v;
+      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(as_pair(a[j], a[j + 1])), "l"(as_pair(b[j], b[j + 1])));
+      from_pair(v, d[j], d[j + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] = a[j] * b[j];
+  }
+}
+// d += a
+template <int V>
+__device__ __forceinline__ void vadd(float (&d)[V], const float (&a)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      uint64_t v;
+      asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(as_pair(d[j], d[j + 1])), "l"(as_pair(a[j], a[j + 1])));
+      from_pair(v, d[j], d[j + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] += a[j];
+  }
+}
+template <int V>
+__device__ __forceinline__ void vset(float (&d)[V], float x) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) d[j] = x;
+}
+template <int V>
+__device__ __forceinline__ float vsum(const float (&a)[V]) {
+  float t = a[0];
+#pragma unroll
+  for (int j = 1; j < V; ++j) t += a[j];
+  return t;
+}
+
 // Sum of v over a row's threads, the same value in each: lanes by butterfly, then (WARP_ROW:
 // a warp has the row to itself) the CTA's warps by another.  The next call that uses `buf` comes
 // after another call's barrier.
@@ -336,52 +405,53 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_kernel(B
     const float gt = gt_next;
     gt_next = token_gate(row + step);
     const int64_t base = row * a.d;
-    float r[NV][V], p[NV][V];
-    float ss = 0.f;
+    float r[NV][V], p[NV][V], k[V], ss[V];
+    vset(ss, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (col(i) < a.d) {
         in.get(0, i, r[i]);
         if (a.y) {
           in.get(1, i, p[i]);
-#pragma unroll
-          for (int j = 0; j < V; ++j) ss = fmaf(p[i][j], p[i][j], ss);
+          vfma(ss, p[i], p[i], ss);
         }
       }
     in.next();
     if (a.y) {
       float s = 1.0f;
       if (a.w_post) {
-        s = __frsqrt_rn(fmaf(row_sum<kWarpRow>(ss, red[odd][0]), inv_d, a.eps));
+        s = __frsqrt_rn(fmaf(row_sum<kWarpRow>(vsum(ss), red[odd][0]), inv_d, a.eps));
         if (tid == 0) a.s_post[row] = s;
       }
-      s *= gt;
+      float b[V];
+      vset(k, s * gt);
+      vset(b, a.beta);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (col(i) < a.d) {
           float w[V];
           par.post(i, col(i), w);
-#pragma unroll
-          for (int j = 0; j < V; ++j) r[i][j] = fmaf(a.beta, r[i][j], p[i][j] * s * w[j]);
+          vmul(p[i], p[i], w);
+          vmul(r[i], r[i], b);
+          vfma(r[i], p[i], k, r[i]);
           RV::store(a.r, base + col(i), r[i]);
         }
     }
     if (a.w_pre) {
-      ss = 0.f;
+      vset(ss, 0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (col(i) < a.d)
-#pragma unroll
-          for (int j = 0; j < V; ++j) ss = fmaf(r[i][j], r[i][j], ss);
-      const float s = __frsqrt_rn(fmaf(row_sum<kWarpRow>(ss, red[odd][1]), inv_d, a.eps));
+        if (col(i) < a.d) vfma(ss, r[i], r[i], ss);
+      const float s = __frsqrt_rn(fmaf(row_sum<kWarpRow>(vsum(ss), red[odd][1]), inv_d, a.eps));
       if (tid == 0) a.s_pre[row] = s;
+      vset(k, s);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (col(i) < a.d) {
           float w[V];
           par.pre(i, col(i), w);
-#pragma unroll
-          for (int j = 0; j < V; ++j) w[j] *= r[i][j] * s;
+          vmul(r[i], r[i], k);
+          vmul(w, w, r[i]);
           RV::store(a.u, base + col(i), w);
         }
     }
@@ -424,7 +494,9 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_bwd_kern
   auto col = [&](int i) { return (tid + i * tpr) * V; };
   int64_t row = kWarpRow ? (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5) : blockIdx.x;
   enum { kR = 0, kDu = 1, kDr = 2, kY = 3 };
-  RowStreams<T, V, NV, 4, norm_rings(V, MAXT), false> in{{a.w_pre ? a.r : nullptr, a.w_pre ? a.du : nullptr, a.dr, a.y}};
+  constexpr bool kRing = norm_rings(V, MAXT);
+  constexpr int kHeld = kRing ? NV : 1;   // accesses whose values are held from one sum to the next
+  RowStreams<T, V, NV, 4, kRing, false> in{{a.w_pre ? a.r : nullptr, a.w_pre ? a.du : nullptr, a.dr, a.y}};
   in.init(ring);
 #pragma unroll
   for (int i = 0; i < kNormRing - 1; ++i) in.ask(row + i * step, a.T, a.d, i, col);
@@ -447,81 +519,92 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_bwd_kern
     post_next = own(a.s_post, a.w_post, row + step);
     gt_next = own(a.gate, a.gate_kind == kGateToken, row + step);
     const int64_t base = row * a.d;
-    float g[NV][V];
-    float mean = 0.f, s = s_pre;
+    float g[NV][V], k[V], t[V], sum[V];
+    // (without the ring the values are read again behind a sum: 1024 threads have 64 registers)
     if (a.w_pre) {
-      float sum = 0.f;
+      float x[kHeld][V], u[kHeld][V];   // xh, du
+      vset(sum, 0.f);
+      vset(k, s_pre);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (col(i) < a.d) {
-          float xh[V], dh[V], w[V];
-          in.get(kR, i, xh);
-          in.get(kDu, i, dh);
+          float w[V];
+          in.get(kR, i, x[kRing ? i : 0]);
+          in.get(kDu, i, u[kRing ? i : 0]);
+          vmul(x[kRing ? i : 0], x[kRing ? i : 0], k);
+          vmul(t, u[kRing ? i : 0], x[kRing ? i : 0]);
+          vadd(acc_pre[i], t);
           par.pre(i, col(i), w);
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float t = dh[j] * (xh[j] * s);
-            acc_pre[i][j] += t;
-            sum = fmaf(t, w[j], sum);
-          }
+          vfma(sum, t, w, sum);
         }
-      mean = row_sum<kWarpRow>(sum, red[odd][0]) * inv_d;
+      const float mean = row_sum<kWarpRow>(vsum(sum), red[odd][0]) * inv_d;
+      float m[V];
+      vset(m, -mean * s_pre);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < a.d) {
+          float w[V];
+          if constexpr (!kRing) {
+            in.get(kR, i, x[kRing ? i : 0]);
+            in.get(kDu, i, u[kRing ? i : 0]);
+            vmul(x[kRing ? i : 0], x[kRing ? i : 0], k);
+          }
+          if (a.dr) in.get(kDr, i, g[i]);
+          else vset(g[i], 0.f);
+          par.pre(i, col(i), w);
+          vmul(w, w, u[kRing ? i : 0]);
+          vfma(g[i], w, k, g[i]);
+          vfma(g[i], x[kRing ? i : 0], m, g[i]);
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < a.d) in.get(kDr, i, g[i]);
     }
+    vset(k, a.beta);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (col(i) < a.d) {
-        if (a.dr) {
-          in.get(kDr, i, g[i]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < V; ++j) g[i][j] = 0.f;
-        }
-        if (a.w_pre) {
-          float xh[V], dh[V], w[V];
-          in.get(kR, i, xh);
-          in.get(kDu, i, dh);
-          par.pre(i, col(i), w);
-#pragma unroll
-          for (int j = 0; j < V; ++j) g[i][j] = fmaf(s, fmaf(-mean, xh[j] * s, dh[j] * w[j]), g[i][j]);
-        }
-        float dx[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) dx[j] = a.beta * g[i][j];
-        RV::store(a.dx, base + col(i), dx);
+        vmul(t, g[i], k);
+        RV::store(a.dx, base + col(i), t);
       }
     if (a.y) {
-      s = s_post;
-      float sum = 0.f;
-      // g becomes g times the channel gate and w_post (q without the token gate)
+      // g becomes q without the token gate: g times post weight and channel gate
+      float y[kHeld][V], ks[V];   // yh
+      vset(sum, 0.f);
+      vset(k, gt);
+      vset(ks, s_post);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (col(i) < a.d) {
-          float yh[V], w[V];
-          in.get(kY, i, yh);
+          float w[V];
+          in.get(kY, i, y[kRing ? i : 0]);
+          vmul(y[kRing ? i : 0], y[kRing ? i : 0], ks);
+          vmul(t, g[i], y[kRing ? i : 0]);
+          vfma(acc_s[i], t, k, acc_s[i]);
           par.post(i, col(i), w);
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            yh[j] *= s;
-            acc_s[i][j] = fmaf(g[i][j] * gt, yh[j], acc_s[i][j]);
-            g[i][j] *= w[j];
-            sum = fmaf(g[i][j], yh[j], sum);
-          }
+          vfma(sum, t, w, sum);
+          vmul(g[i], g[i], w);
         }
-      mean = 0.f;
+      float mean = 0.f;
       if (a.w_post || a.gate_kind == kGateToken) {   // the same for every thread
-        sum = row_sum<kWarpRow>(sum, red[odd][1]);
-        if (a.gate_kind == kGateToken && tid == 0) a.d_gate_tok[row] = sum;
-        if (a.w_post) mean = sum * inv_d;
+        mean = row_sum<kWarpRow>(vsum(sum), red[odd][1]);
+        if (a.gate_kind == kGateToken && tid == 0) a.d_gate_tok[row] = mean;
+        mean = a.w_post ? mean * inv_d : 0.f;
       }
-      const float sg = s * gt;
+      float m[V];
+      vset(k, s_post * gt);
+      vset(m, -mean * (s_post * gt));
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (col(i) < a.d) {
-          float yh[V];
-          in.get(kY, i, yh);
-#pragma unroll
-          for (int j = 0; j < V; ++j) yh[j] = sg * fmaf(-mean, yh[j] * s, g[i][j]);
-          RV::store(a.dy, base + col(i), yh);
+          if constexpr (!kRing) {
+            in.get(kY, i, y[kRing ? i : 0]);
+            vmul(y[kRing ? i : 0], y[kRing ? i : 0], ks);
+          }
+          vmul(g[i], g[i], k);
+          vfma(g[i], y[kRing ? i : 0], m, g[i]);
+          RV::store(a.dy, base + col(i), g[i]);
         }
     }
     in.next();

@@ -30,9 +30,11 @@ cudaError_t with_row_shape(int d, bool vec, F&& f) {
     if (n <= 64) return f(Int<V>{}, Int<2>{}, Int<32>{}, 32 * kNormWarps, kNormWarps);
     if (n <= NV * 256) return f(Int<V>{}, Int<NV>{}, Int<256>{}, threads((n + NV - 1) / NV), 1);
     if (n <= NV * 512) return f(Int<V>{}, Int<NV>{}, Int<512>{}, threads((n + NV - 1) / NV), 1);
-    if (BWD && n <= 1024) return f(Int<V>{}, Int<1>{}, Int<1024>{}, threads(n), 1);
-    if (n <= 2048) return f(Int<V>{}, Int<2>{}, Int<1024>{}, threads((n + 1) / 2), 1);
-    return f(Int<V>{}, Int<4>{}, Int<1024>{}, threads((n + 3) / 4), 1);
+    if constexpr (BWD)
+      if (n <= 1024) return f(Int<V>{}, Int<1>{}, Int<1024>{}, threads(n), 1);
+    if constexpr (V < 8)   // (kNormMaxD is 2048 accesses of 8)
+      if (n > 2048) return f(Int<V>{}, Int<4>{}, Int<1024>{}, threads((n + 3) / 4), 1);
+    return f(Int<V>{}, Int<2>{}, Int<1024>{}, threads((n + 1) / 2), 1);
   }
   if (d <= 256) return f(Int<1>{}, Int<8>{}, Int<32>{}, 32 * kNormWarps, kNormWarps);
   if (d <= 2048) return f(Int<1>{}, Int<8>{}, Int<256>{}, threads((d + 7) / 8), 1);
