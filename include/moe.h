@@ -302,7 +302,8 @@ void moe_ep_destroy(moe_ep_handle* handle);
  *   moe_grouped_mm        y[r, :]  = x[r, :] W_e^T
  *   moe_grouped_mm_dgrad  dx[r, :] = dy[r, :] W_e
  *   moe_grouped_mm_wgrad  dw_e     = dy_e^T x_e (fp32; 0 for an expert without rows), or
- *                         dw_e    += dy_e^T x_e with accumulate != 0
+ *                         dw_e    += dy_e^T x_e with accumulate != 0 (the product rounded to
+ *                         fp32, then the sum; a subnormal sum may become 0)
  * x, dx [rows, k]; y, dy [rows, n]; w [n_groups, n, k]; dw [n_groups, n, k] fp32; the rest in
  * dtype (MOE_BF16 or MOE_FP32), products accumulated in fp32 and rounded once.
  * counts [n_groups] int32; all pointers DEVICE.  rows is the buffers' capacity: rows behind
@@ -314,7 +315,7 @@ void moe_ep_destroy(moe_ep_handle* handle);
  * (0, then NULL, unless a weight gradient with few tiles and many rows is split over its rows),
  * free again when the call's work is done.  No allocation, no host synchronisation; deterministic.
  * Each result depends only on its own expert's rows (infinities and NaNs of other rows do
- * not reach it).  */
+ * not reach it). */
 moe_status moe_grouped_mm(const void* x, const void* w, const int32_t* counts, int32_t n_groups,
                           int64_t rows, int32_t n, int32_t k, int32_t dtype, void* y,
                           moe_stream_t stream);
@@ -350,8 +351,9 @@ moe_status moe_grouped_device_status(moe_stream_t stream);
  * forward's; without y, dx is the gradient of x = r.  workspace: 16-byte aligned DEVICE
  * memory of moe_block_norm_workspace(T, d) bytes, free again when the call's work is done.
  * 0 <= T < 2^31, 1 <= d <= 16384, eps > 0.  r and u may each be x or y itself (not both the
- * same one), dx and dy each one of y, r, dr, du; other overlaps are refused.  No allocation,
- * no host synchronisation; deterministic (fixed-order sums, no atomics). */
+ * same one), dx and dy each one of y, r, dr, du; other overlaps of what is written with
+ * what is read or written are refused.  No allocation, no host
+ * synchronisation; deterministic (fixed-order sums, no atomics). */
 typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_gate_kind;
 moe_status moe_block_norm(const void* x, const void* y, const float* gate, int32_t gate_kind,
                           const float* post_weight, const float* pre_weight, int64_t T, int32_t d,

@@ -149,6 +149,11 @@ moe_status moe_block_norm(const void* x, const void* y, const float* gate, int32
     for (const void* i : {x, y})
       if (o != i && overlaps(o, bytes, i, bytes))
         return fail(MOE_ERR_INVALID_ARG, "an output overlaps an input without being the same buffer");
+  const size_t tok = (size_t)T * 4, ch = (size_t)d * 4;
+  if (!apart({{post_rstd, tok}, {pre_rstd, tok}},
+             {{x, bytes}, {y, bytes}, {r, bytes}, {u, bytes}, {post_weight, ch}, {pre_weight, ch},
+              {gate, gate_kind == kGateToken ? tok : ch}}))
+    return fail(MOE_ERR_INVALID_ARG, "a statistic overlaps another buffer");
   int n_sms = 0, device = 0;
   MOE_TRY(op_device(&n_sms, &device));
   BlockNormArgs a{x, y, gate, post_weight, pre_weight, r, u, post_rstd, pre_rstd, T, d, gate_kind, beta, eps};
@@ -198,6 +203,11 @@ moe_status moe_block_norm_backward(const void* y, const void* r, const void* dr,
         return fail(MOE_ERR_INVALID_ARG, "an output overlaps an input without being the same buffer");
   if (!workspace || !aligned16(workspace) || workspace_bytes < moe_block_norm_workspace(T, d))
     return fail(MOE_ERR_INVALID_ARG, "workspace must be 16-byte aligned and hold moe_block_norm_workspace bytes");
+  const size_t tok = (size_t)T * 4, ch = (size_t)d * 4, gb = gate_kind == kGateToken ? tok : ch;
+  if (!apart({{d_gate, gb}, {d_post_weight, ch}, {d_pre_weight, ch}, {workspace, moe_block_norm_workspace(T, d)}},
+             {{y, bytes}, {r, bytes}, {dr, bytes}, {du, bytes}, {dx, bytes}, {dy, bytes}, {post_rstd, tok},
+              {pre_rstd, tok}, {gate, gb}, {post_weight, ch}, {pre_weight, ch}}))
+    return fail(MOE_ERR_INVALID_ARG, "a parameter's gradient or the workspace overlaps another buffer");
   int n_sms = 0, device = 0;
   MOE_TRY(op_device(&n_sms, &device));
   const bool need_s = post_weight || channel;

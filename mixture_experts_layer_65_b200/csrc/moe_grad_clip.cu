@@ -14,12 +14,12 @@ namespace {
 // listed twice would be scaled twice, in no order).
 moe_status check_disjoint(const void* const* grads, void* const* outs, const int64_t* numels,
                           const int32_t* dtypes, int n) {
-  struct Span {
+  struct Range {
     uintptr_t lo, hi;
     int tensor;
     bool out;
   };
-  std::vector<Span> spans;
+  std::vector<Range> spans;
   try {
     spans.reserve(2 * (size_t)n);
   } catch (const std::bad_alloc&) {
@@ -29,14 +29,14 @@ moe_status check_disjoint(const void* const* grads, void* const* outs, const int
     if (numels[i] == 0) continue;
     const size_t bytes = (size_t)numels[i] * (dtypes[i] == MOE_BF16 ? 2 : 4);
     const uintptr_t o = reinterpret_cast<uintptr_t>(outs[i]), g = reinterpret_cast<uintptr_t>(grads[i]);
-    spans.push_back(Span{o, o + bytes, i, true});
-    if (g != o) spans.push_back(Span{g, g + bytes, i, false});
+    spans.push_back(Range{o, o + bytes, i, true});
+    if (g != o) spans.push_back(Range{g, g + bytes, i, false});
   }
-  auto before = [](const Span& a, const Span& b) { return a.lo < b.lo; };
+  auto before = [](const Range& a, const Range& b) { return a.lo < b.lo; };
   if (!std::is_sorted(spans.begin(), spans.end(), before)) std::sort(spans.begin(), spans.end(), before);
   // in order of their starts: the furthest end so far of the outputs and of all spans
   uintptr_t out_end = 0, end = 0;
-  for (const Span& s : spans) {
+  for (const Range& s : spans) {
     if (s.lo < out_end || (s.out && s.lo < end))
       return fail(MOE_ERR_INVALID_ARG, "tensor %d shares memory with another tensor's output", s.tensor);
     if (s.out) out_end = std::max(out_end, s.hi);

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <atomic>
+#include <initializer_list>
 
 #include "api_common.cuh"
 
@@ -36,6 +37,22 @@ inline bool overlaps(const void* p, size_t n, const void* q, size_t m) {
   if (!p || !q || n == 0 || m == 0) return false;
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   return a < b + m && b < a + n;
+}
+
+// A buffer a call reads or writes (nullptr or 0 bytes: none).
+struct Span {
+  const void* p;
+  size_t n;
+};
+// Whether every output is apart from all inputs and from the outputs before it.
+inline bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (overlaps(o->p, o->n, i.p, i.n)) return false;
+    for (const Span* q = outs.begin(); q != o; ++q)
+      if (overlaps(o->p, o->n, q->p, q->n)) return false;
+  }
+  return true;
 }
 
 inline bool misaligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }

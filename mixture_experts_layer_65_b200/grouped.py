@@ -97,6 +97,8 @@ def grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, counts: torch.Tensor,
 def device_status(device=None, stream: torch.cuda.Stream | None = None) -> None:
     """Synchronise `stream` (default: the current stream of `device`) and raise if a grouped
     product on that device recorded a device-side error."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    dev = torch.device("cuda" if device is None else device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
     with on_stream(dev, stream) as s:
         check(lib().moe_grouped_device_status(s))

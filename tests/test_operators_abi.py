@@ -59,8 +59,9 @@ def test_split_weight_gradients_want_their_workspace(L):
     assert L.moe_grouped_wgrad_workspace(2, 0, 64, 64, 1) == 0
 
 
+E = 5 << 40
 NORM = dict(x=A, y=B, gate=None, kind=0, post=C, pre=C, T=8, d=64, dtype=_lib.MOE_BF16, beta=1.0, eps=1e-6,
-            r=D, u=D + (1 << 30), ps=C, qs=C)
+            r=D, u=D + (1 << 30), ps=E, qs=E + 4096)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -70,7 +71,7 @@ NORM = dict(x=A, y=B, gate=None, kind=0, post=C, pre=C, T=8, d=64, dtype=_lib.MO
     (dict(dtype=3), BAD), (dict(kind=3), BAD), (dict(kind=1), BAD), (dict(gate=C), BAD),
     (dict(eps=0.0), BAD), (dict(eps=float("nan")), BAD), (dict(eps=float("inf")), BAD),
     (dict(beta=float("inf")), BAD), (dict(x=A + 1), BAD), (dict(u=D), BAD), (dict(u=D + 16), BAD),
-    (dict(r=A + 128), BAD), (dict(u=B + 2), BAD),
+    (dict(r=A + 128), BAD), (dict(u=B + 2), BAD), (dict(ps=C), BAD), (dict(qs=E + 4), BAD), (dict(qs=D + 64), BAD),
     (dict(y=None, r=None, post=None, ps=None, beta=2.0), BAD),
     (dict(y=None, r=None, post=None, ps=None, gate=C, kind=1), BAD),
     (dict(y=None, r=None, post=None, ps=None, pre=None, u=None, qs=None), BAD),
@@ -83,14 +84,16 @@ def test_block_norm_refuses(L, kw, status):
 
 
 BWD = dict(y=A, r=B, dr=C, du=C + (1 << 30), gate=None, kind=0, post=C, pre=C, ps=C, qs=C, T=8, d=64,
-           dtype=_lib.MOE_FP32, beta=1.0, dx=D, dy=D + (1 << 30), dg=None, dpost=A, dpre=A, ws=A, size=1 << 20)
+           dtype=_lib.MOE_FP32, beta=1.0, dx=D, dy=D + (1 << 30), dg=None, dpost=E, dpre=E + 4096, ws=E + 8192,
+           size=1 << 20)
 
 
 @pytest.mark.parametrize("kw", [
     dict(r=None), dict(du=None), dict(dx=None), dict(dy=None), dict(y=None), dict(ps=None), dict(qs=None),
-    dict(dpost=None), dict(dpre=None), dict(dg=A), dict(ws=None), dict(size=8 * 64 * 8 - 1), dict(ws=A + 4),
+    dict(dpost=None), dict(dpre=None), dict(dg=A), dict(ws=None), dict(size=8 * 64 * 8 - 1), dict(ws=E + 8196),
     dict(pre=None, du=None, qs=None, dpre=None, dr=None), dict(dx=B + 4), dict(dy=D + 8), dict(dy=D),
     dict(kind=1, gate=C), dict(d=0), dict(dtype=9), dict(beta=float("nan")),
+    dict(dpost=C), dict(dpre=E), dict(ws=E), dict(ws=D + 16), dict(kind=2, gate=E + (1 << 20), dg=E + (1 << 20)),
 ])
 def test_block_norm_backward_refuses(L, kw):
     v = {**BWD, **kw}
