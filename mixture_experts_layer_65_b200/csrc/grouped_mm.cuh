@@ -176,22 +176,32 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 //   mm:    A[m, q] = x[row0 + m][q]       B[n, q] = W[n][q]      q < K
 //   dgrad: A[m, q] = dy[row0 + m][q]      B[n, q] = W[q][n]      q < N
 //   wgrad: A[m, q] = dy[row0 + q][m]      B[n, q] = x[row0 + q][n]   q < rows of the group
-template <int OP, int BM, int BN, int R, int V>
-__global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(GroupedSimtArgs p) {
-  constexpr int kThreads = BM * BN / (R * R);
+// KS > 1: the CTA has KS such sets of threads, each with its own buffers and every KS-th step of the
+// contraction; the sets' sums meet in shared memory, added in order.
+template <int OP, int BM, int BN, int R, int V, int KS>
+__global__ void __launch_bounds__(BM * BN / (R * R) * KS, KS > 1 ? 2 : 1) grouped_simt_kernel(GroupedSimtArgs p) {
+  constexpr int kThreads = BM * BN / (R * R);   // of a set
   constexpr int kA = BM * kGsBK / kThreads / V, kB = BN * kGsBK / kThreads / V;   // loads of a thread
   constexpr bool W = OP == kGroupedWgrad;
   pdl_launch_dependents();
   pdl_wait();
   __shared__ GroupTable tab;
-  __shared__ __align__(16) float As[2][kGsBK][BM + 4];
-  __shared__ __align__(16) float Bs[2][kGsBK][BN + 4];
+  __shared__ __align__(16) float Asets[KS][2][kGsBK][BM + 4];
+  __shared__ __align__(16) float Bsets[KS][2][kGsBK][BN + 4];
+  static_assert(KS == 1 || sizeof(Asets) >= sizeof(float) * (KS - 1) * kThreads * R * R, "the sums' meeting place");
+  const int set = threadIdx.x / kThreads;
+  auto& As = Asets[set];
+  auto& Bs = Bsets[set];
+  auto set_sync = [&] {
+    if constexpr (KS == 1) __syncthreads();
+    else named_bar_sync(1 + set, kThreads);
+  };
   const int out_cols = OP == kGroupedMM ? p.N : p.K;
   const int nt = (out_cols + BN - 1) / BN;
   const int mt_w = (p.N + BM - 1) / BM;   // row tiles of a weight gradient
   group_table(tab, p.counts, p.G, p.rows, W ? 0 : BM, W ? nt * mt_w * p.splits : nt);
   const int total = tab.tile0[p.G];
-  const int tid = threadIdx.x, tx = tid % (BN / R), ty = tid / (BN / R);
+  const int tid = threadIdx.x % kThreads, tx = tid % (BN / R), ty = tid / (BN / R);
   const int lda = OP == kGroupedMM ? p.K : p.N;
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
     const int g = group_of(tab, p.G, tile);
@@ -256,15 +266,15 @@ __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(Grouped
 #pragma unroll
       for (int j = 0; j < R / 2; ++j) acc[i][j] = sum[i][j] = make_float2(0.f, 0.f);
     constexpr int kRunM = BM / (R / 4), kRunN = BN / (R / 4);
-    if (Q > 0) {
-      fetch(0);
-      __syncthreads();   // the previous tile's last step has been read
+    __syncthreads();   // the previous tile's last step, and its sums, have been read
+    if (set * kGsBK < Q) {
+      fetch(set * kGsBK);
       put(0);
-      __syncthreads();
+      set_sync();
       int buf = 0, steps = 0;
-      for (int q0 = 0; q0 < Q; q0 += kGsBK, buf ^= 1) {
-        const bool more = q0 + kGsBK < Q;
-        if (more) fetch(q0 + kGsBK);
+      for (int q0 = set * kGsBK; q0 < Q; q0 += KS * kGsBK, buf ^= 1) {
+        const bool more = q0 + KS * kGsBK < Q;
+        if (more) fetch(q0 + KS * kGsBK);
 #pragma unroll
         for (int q = 0; q < kGsBK; ++q) {
           float av[R];
@@ -292,9 +302,35 @@ __global__ void __launch_bounds__(BM * BN / (R * R)) grouped_simt_kernel(Grouped
         }
         if (more) {
           put(buf ^ 1);
-          __syncthreads();
+          set_sync();
         }
       }
+    }
+    if constexpr (KS > 1) {
+      float* meet = &Asets[0][0][0][0];
+      __syncthreads();   // every set is done with its buffers
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < R / 2; ++j) {
+          sum[i][j].x += acc[i][j].x;
+          sum[i][j].y += acc[i][j].y;
+          acc[i][j] = make_float2(0.f, 0.f);
+          if (set > 0)
+            *reinterpret_cast<float2*>(meet + (((set - 1) * R * R + i * R + 2 * j) * kThreads) + 2 * tid) = sum[i][j];
+        }
+      __syncthreads();
+      if (set > 0) continue;
+#pragma unroll
+      for (int k = 0; k < KS - 1; ++k)
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int j = 0; j < R / 2; ++j) {
+            const float2 x = *reinterpret_cast<const float2*>(meet + ((k * R * R + i * R + 2 * j) * kThreads) + 2 * tid);
+            sum[i][j].x += x.x;
+            sum[i][j].y += x.y;
+          }
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {

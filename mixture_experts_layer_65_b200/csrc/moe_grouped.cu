@@ -42,26 +42,27 @@ int64_t tiles_of(const Shape& s, int bm, int bn) {
 }
 
 // fp32.  The largest tiles that give every SM two CTAs of 128 x 128 or three of 64 x 64; small
-// problems take 32 x 32, one element a load (16-byte loads turned into K-major rows of so small a
+// problems take 32 x 32, the contraction over four sets of threads (one
+// expert of 384 rows, 1024 x 1024: 68 us -> 45), one element a load (16-byte loads turned into K-major rows of so small a
 // tile cost more than they save: 60 experts of 25 rows, 200 x 332, 27 us against 41; on larger
 // tiles they save: 4 experts of 500 rows, 1000 x 1000, 126 us against 155).
-template <int OP, int BM, int BN, int R, int V>
+template <int OP, int BM, int BN, int R, int V, int KS>
 cudaError_t launch_simt_tile(const GroupedSimtArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
-  constexpr int kThreads = BM * BN / (R * R);
+  constexpr int kThreads = BM * BN / (R * R) * KS;
   const int64_t tiles = a.splits * tiles_of<OP>(s, BM, BN), most = (int64_t)n_sms * (1024 / kThreads);
-  return launch_pdl(grouped_simt_kernel<OP, BM, BN, R, V>, dim3((unsigned)(tiles < most ? tiles : most)),
+  return launch_pdl(grouped_simt_kernel<OP, BM, BN, R, V, KS>, dim3((unsigned)(tiles < most ? tiles : most)),
                     dim3(kThreads), 0, st, a);
 }
 template <int OP>
 cudaError_t launch_simt(const GroupedSimtArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
   const bool v4 = s.n % 4 == 0 && s.k % 4 == 0 && aligned16(a.a) && aligned16(a.b);
   if (a.splits * tiles_of<OP>(s, 128, 128) >= 2 * n_sms)
-    return v4 ? launch_simt_tile<OP, 128, 128, 8, 4>(a, s, n_sms, st)
-              : launch_simt_tile<OP, 128, 128, 8, 1>(a, s, n_sms, st);
+    return v4 ? launch_simt_tile<OP, 128, 128, 8, 4, 1>(a, s, n_sms, st)
+              : launch_simt_tile<OP, 128, 128, 8, 1, 1>(a, s, n_sms, st);
   if (a.splits * tiles_of<OP>(s, 64, 64) >= 3 * n_sms)
-    return v4 ? launch_simt_tile<OP, 64, 64, 8, 4>(a, s, n_sms, st)
-              : launch_simt_tile<OP, 64, 64, 8, 1>(a, s, n_sms, st);
-  return launch_simt_tile<OP, 32, 32, 4, 1>(a, s, n_sms, st);
+    return v4 ? launch_simt_tile<OP, 64, 64, 8, 4, 1>(a, s, n_sms, st)
+              : launch_simt_tile<OP, 64, 64, 8, 1, 1>(a, s, n_sms, st);
+  return launch_simt_tile<OP, 32, 32, 4, 1, 4>(a, s, n_sms, st);
 }
 
 // bf16 that TMA cannot take.
