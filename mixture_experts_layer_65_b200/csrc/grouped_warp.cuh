@@ -8,6 +8,9 @@
 // one whose output index is as [contraction][output], read with ldmatrix and ldmatrix.trans
 // (16-byte chunks swizzled, or rows padded by 16 bytes, so that the reads do not meet in a bank).
 // wgrad adds up its accumulators in registers every kGwpChunk steps (see grouped_wgrad.cuh).
+//
+// Bound by the element-wise loads: 8 experts of 1000 rows, 1001 x 2003: mm 464 us, dgrad 358, wgrad
+// 423 (69 to 90 TFLOP/s; the FMA kernel 1210, 970, 1063).
 #pragma once
 
 #include "grouped_mm.cuh"

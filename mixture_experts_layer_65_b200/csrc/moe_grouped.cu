@@ -42,10 +42,10 @@ int64_t tiles_of(const Shape& s, int bm, int bn) {
 }
 
 // fp32.  The largest tiles that give every SM two CTAs of 128 x 128 or three of 64 x 64; small
-// problems take 32 x 32, the contraction over four sets of threads (one
-// expert of 384 rows, 1024 x 1024: 68 us -> 45), one element a load (16-byte loads turned into K-major rows of so small a
-// tile cost more than they save: 60 experts of 25 rows, 200 x 332, 27 us against 41; on larger
-// tiles they save: 4 experts of 500 rows, 1000 x 1000, 126 us against 155).
+// problems take 32 x 32 with the contraction over four sets of threads (one expert of 384 rows,
+// 1024 x 1024: 68 us -> 45) and one element a load (16-byte loads turned into K-major rows of so
+// small a tile cost more than they save: 60 experts of 25 rows, 200 x 332, 27 us against 41; on
+// larger tiles they save: 4 experts of 500 rows, 1000 x 1000, 126 us against 155).
 template <int OP, int BM, int BN, int R, int V, int KS>
 cudaError_t launch_simt_tile(const GroupedSimtArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
   constexpr int kThreads = BM * BN / (R * R) * KS;
@@ -65,7 +65,7 @@ cudaError_t launch_simt(const GroupedSimtArgs& a, const Shape& s, int n_sms, cud
   return launch_simt_tile<OP, 32, 32, 4, 1, 4>(a, s, n_sms, st);
 }
 
-// bf16 that TMA cannot take.
+// bf16 that TMA cannot take: 64 x 64 tiles where 128 x 128 would not give every SM one.
 template <int OP, int BM, int BN, int WM, int WN>
 cudaError_t launch_warp_tile(const GroupedWarpArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
   constexpr int kThreads = (BM / WM) * (BN / WN) * 32;
@@ -142,8 +142,10 @@ bool takes_tma(const Shape& s, const void* a, const void* b, const void* out) {
          aligned16(out);
 }
 
-// Parts of a weight gradient's rows: by the tiles of the kernel that runs it.  (Slots and tile
-// sizes are those of a B200's 148 SMs, so that the workspace's size needs no device.)
+// Parts of a weight gradient's rows: by the tiles of the kernel that runs it.  (Slots are those of
+// a B200's 148 SMs, so that the workspace's size needs no device.)  One expert of 100,000 rows,
+// 64 x 64: 28 us in 74 parts, 0.5 ms in one; 72 tiles for 74 slots stay whole (split in two,
+// 796 us against 478 for 65,536 rows).
 int splits_of(const Shape& s, bool tma) {
   constexpr int kSms = 148;
   if (tma) return wgrad_splits(s.rows, s.G, tiles_of<kGroupedWgrad>(s, kPairBM, kGemmBN), kSms / 2, 1024);
