@@ -308,7 +308,7 @@ void moe_ep_destroy(moe_ep_handle* handle);
  * dtype (MOE_BF16 or MOE_FP32), products accumulated in fp32 and rounded once.
  * counts [n_groups] int32; all pointers DEVICE.  rows is the buffers' capacity: rows behind
  * the last expert's are not read into any result and not written; a negative count counts as
- * 0, and rows that counts claims past `rows` are ignored.  1 <= n_groups <= 1024, rows < 2^30
+ * 0, and rows that counts claims past `rows` are ignored.  1 <= n_groups <= 1024, rows < 2^28
  * (0 allowed), any n and k up to 2^20; bf16 products with n and k multiples of 8 and 16-byte
  * aligned buffers are read by TMA, other bf16 ones element by element.  An output may not
  * overlap an input.  workspace: moe_grouped_wgrad_workspace bytes of 16-byte aligned DEVICE memory
@@ -376,9 +376,11 @@ moe_status moe_block_norm_backward(const void* y, const void* r, const void* dr,
  * their type), element counts (0 allowed), MOE_FP32 or MOE_BF16 each; they are read during
  * the call only.  outs[i] is grads[i] itself (in place) or a buffer that overlaps none of the
  * others; the same buffer twice among the outputs is refused.  Squares and sums are 64-bit,
- * in an order fixed by the sizes.  When N <= max_norm, or N is not finite, the coefficient is
- * 1: gradients in place stay untouched, and the caller sees N.  workspace: 8-byte aligned
- * DEVICE memory of moe_grad_workspace(n_tensors) bytes, free again when the call's work is done.
+ * in an order fixed by the sizes.  When N <= max_norm, or N is not finite (a gradient is not),
+ * the coefficient is 1: gradients in place stay untouched, and the caller sees N (an fp32 norm
+ * reads infinite too when a finite N is past 2^128; the gradients are then scaled by max_norm / N).
+ * workspace: 8-byte aligned DEVICE memory of moe_grad_workspace(n_tensors) bytes, free again when
+ * the call's work is done.  sumsq, norm and the workspace may not overlap each other or a tensor.
  *   moe_clip_grad_norm  both steps; norm [1] fp32 (DEVICE) = N
  *   moe_grad_sumsq      sum of g^2 to sumsq [1] (fp64) and/or its root to norm [1] (fp32)
  *   moe_grad_scale      the second step for a given sumsq [1] (e.g. summed over ranks whose

@@ -154,6 +154,9 @@ moe_status moe_block_norm(const void* x, const void* y, const float* gate, int32
              {{x, bytes}, {y, bytes}, {r, bytes}, {u, bytes}, {post_weight, ch}, {pre_weight, ch},
               {gate, gate_kind == kGateToken ? tok : ch}}))
     return fail(MOE_ERR_INVALID_ARG, "a statistic overlaps another buffer");
+  if (!apart({{r, bytes}, {u, bytes}},
+             {{post_weight, ch}, {pre_weight, ch}, {gate, gate_kind == kGateToken ? tok : ch}}))
+    return fail(MOE_ERR_INVALID_ARG, "r or u overlaps a parameter");
   int n_sms = 0, device = 0;
   MOE_TRY(op_device(&n_sms, &device));
   BlockNormArgs a{x, y, gate, post_weight, pre_weight, r, u, post_rstd, pre_rstd, T, d, gate_kind, beta, eps};
@@ -208,6 +211,9 @@ moe_status moe_block_norm_backward(const void* y, const void* r, const void* dr,
              {{y, bytes}, {r, bytes}, {dr, bytes}, {du, bytes}, {dx, bytes}, {dy, bytes}, {post_rstd, tok},
               {pre_rstd, tok}, {gate, gb}, {post_weight, ch}, {pre_weight, ch}}))
     return fail(MOE_ERR_INVALID_ARG, "a parameter's gradient or the workspace overlaps another buffer");
+  if (!apart({{dx, bytes}, {dy, bytes}},
+             {{post_rstd, tok}, {pre_rstd, tok}, {gate, gb}, {post_weight, ch}, {pre_weight, ch}}))
+    return fail(MOE_ERR_INVALID_ARG, "dx or dy overlaps a parameter or a statistic");
   int n_sms = 0, device = 0;
   MOE_TRY(op_device(&n_sms, &device));
   const bool need_s = post_weight || channel;

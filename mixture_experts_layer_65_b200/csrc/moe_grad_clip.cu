@@ -45,10 +45,12 @@ moe_status check_disjoint(const void* const* grads, void* const* outs, const int
   return MOE_OK;
 }
 
+// `own`: what the call reads and writes besides the tensors, apart from them and from each other.
 moe_status check_tensors(const void* const* grads, void* const* outs, const int64_t* numels,
-                         const int32_t* dtypes, int32_t n) {
+                         const int32_t* dtypes, int32_t n, std::initializer_list<Span> own) {
   if (n < 0) return fail(MOE_ERR_INVALID_ARG, "n_tensors must not be negative");
   if (n > 0 && (!grads || !numels || !dtypes)) return fail(MOE_ERR_INVALID_ARG, "a table pointer is NULL");
+  if (!apart(own, {})) return fail(MOE_ERR_INVALID_ARG, "sumsq, norm and workspace overlap");
   int64_t chunks = 0;
   for (int i = 0; i < n; ++i) {
     if (dtypes[i] != MOE_BF16 && dtypes[i] != MOE_FP32)
@@ -56,12 +58,15 @@ moe_status check_tensors(const void* const* grads, void* const* outs, const int6
     if (numels[i] < 0 || numels[i] >= (int64_t(1) << 40))
       return fail(MOE_ERR_INVALID_ARG, "tensor %d: %lld elements", i, (long long)numels[i]);
     if (numels[i] == 0) continue;
-    const size_t es = dtypes[i] == MOE_BF16 ? 2 : 4;
+    const size_t es = dtypes[i] == MOE_BF16 ? 2 : 4, bytes = (size_t)numels[i] * es;
     if (!grads[i] || (outs && !outs[i])) return fail(MOE_ERR_INVALID_ARG, "tensor %d: NULL pointer", i);
     if (misaligned(grads[i], es) || (outs && misaligned(outs[i], es)))
       return fail(MOE_ERR_INVALID_ARG, "tensor %d is not aligned to its type", i);
-    if (outs && outs[i] != grads[i] && overlaps(outs[i], (size_t)numels[i] * es, grads[i], (size_t)numels[i] * es))
+    if (outs && outs[i] != grads[i] && overlaps(outs[i], bytes, grads[i], bytes))
       return fail(MOE_ERR_INVALID_ARG, "tensor %d overlaps its output without being the same buffer", i);
+    for (const Span& o : own)
+      if (overlaps(o.p, o.n, grads[i], bytes) || (outs && overlaps(o.p, o.n, outs[i], bytes)))
+        return fail(MOE_ERR_INVALID_ARG, "tensor %d overlaps sumsq, norm or the workspace", i);
     chunks += (numels[i] + kClipChunk - 1) / kClipChunk;
   }
   if (chunks >= (int64_t(1) << 31)) return fail(MOE_ERR_UNSUPPORTED, "too many elements in one call");
@@ -144,7 +149,8 @@ size_t moe_grad_workspace(int32_t n_tensors) {
 moe_status moe_grad_sumsq(const void* const* grads, const int64_t* numels, const int32_t* dtypes,
                           int32_t n_tensors, double* sumsq, float* norm, void* workspace,
                           size_t workspace_bytes, moe_stream_t stream) {
-  MOE_TRY(check_tensors(grads, nullptr, numels, dtypes, n_tensors));
+  MOE_TRY(check_tensors(grads, nullptr, numels, dtypes, n_tensors,
+                        {{sumsq, 8}, {norm, 4}, {workspace, moe_grad_workspace(n_tensors)}}));
   if (!sumsq && !norm) return fail(MOE_ERR_INVALID_ARG, "neither sumsq nor norm is given");
   MOE_TRY(check_workspace(workspace, workspace_bytes, n_tensors));
   int n_sms = 0, sums = 0;
@@ -164,7 +170,7 @@ moe_status moe_grad_scale(const void* const* grads, void* const* outs, const int
                           const int32_t* dtypes, int32_t n_tensors, const double* sumsq, float max_norm,
                           float* norm, moe_stream_t stream) {
   if (n_tensors > 0 && !outs) return fail(MOE_ERR_INVALID_ARG, "a table pointer is NULL");
-  MOE_TRY(check_tensors(grads, outs, numels, dtypes, n_tensors));
+  MOE_TRY(check_tensors(grads, outs, numels, dtypes, n_tensors, {{sumsq, 8}, {norm, 4}}));
   if (!sumsq) return fail(MOE_ERR_INVALID_ARG, "sumsq is NULL");
   if (!(max_norm >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "max_norm must not be negative or NaN");
   int n_sms = 0;
@@ -186,7 +192,8 @@ moe_status moe_clip_grad_norm(const void* const* grads, void* const* outs, const
                               const int32_t* dtypes, int32_t n_tensors, float max_norm, float* norm,
                               void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   if (n_tensors > 0 && !outs) return fail(MOE_ERR_INVALID_ARG, "a table pointer is NULL");
-  MOE_TRY(check_tensors(grads, outs, numels, dtypes, n_tensors));
+  MOE_TRY(check_tensors(grads, outs, numels, dtypes, n_tensors,
+                        {{norm, 4}, {workspace, moe_grad_workspace(n_tensors)}}));
   if (!norm) return fail(MOE_ERR_INVALID_ARG, "norm is NULL");
   if (!(max_norm >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "max_norm must not be negative or NaN");
   MOE_TRY(check_workspace(workspace, workspace_bytes, n_tensors));

@@ -24,7 +24,9 @@ moe_status check_shape(const Shape& s) {
   if (s.n < 1 || s.k < 1) return fail(MOE_ERR_INVALID_ARG, "n and k must be positive");
   if (s.n > (1 << 20) || s.k > (1 << 20)) return fail(MOE_ERR_UNSUPPORTED, "n=%d or k=%d above 2^20", s.n, s.k);
   if (s.rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows must not be negative");
-  if (s.rows >= (int64_t(1) << 30)) return fail(MOE_ERR_UNSUPPORTED, "rows=%lld above 2^30", (long long)s.rows);
+  // (one tile of a weight gradient whose expert has all the rows has to end well within the
+  // kernels' bounded waits: 2^28 rows are 2^21 stages of at most half a microsecond)
+  if (s.rows >= (int64_t(1) << 28)) return fail(MOE_ERR_UNSUPPORTED, "rows=%lld not below 2^28", (long long)s.rows);
   // tiles of the smallest kind, all groups together, are counted in 32 bits
   const int64_t nt = (s.n + 31) / 32, kt = (s.k + 31) / 32;
   const int64_t mt = (s.rows + 31) / 32 + s.G;

@@ -27,7 +27,7 @@ GROUPED = dict(a=A, b=B, counts=C, g=4, rows=64, n=64, k=64, dtype=_lib.MOE_BF16
     (dict(n=0), BAD), (dict(k=-3), BAD), (dict(n=(1 << 20) + 1), UNSUP), (dict(dtype=2), BAD),
     (dict(dtype=7), BAD), (dict(a=A + 1), BAD), (dict(counts=C + 2), BAD),
     (dict(out=A), BAD), (dict(out=A + 64), BAD), (dict(out=B + 128), BAD), (dict(counts=D + 4), BAD),
-    (dict(rows=(1 << 30) - 1, n=1 << 20), UNSUP),
+    (dict(rows=(1 << 30) - 1, n=1 << 20), UNSUP), (dict(rows=1 << 28), UNSUP), (dict(rows=(1 << 28) - 1, a=None), BAD),
 ])
 @pytest.mark.parametrize("op", ["moe_grouped_mm", "moe_grouped_mm_dgrad", "moe_grouped_mm_wgrad"])
 def test_grouped_products_refuse(L, op, kw, status):
@@ -72,6 +72,7 @@ NORM = dict(x=A, y=B, gate=None, kind=0, post=C, pre=C, T=8, d=64, dtype=_lib.MO
     (dict(eps=0.0), BAD), (dict(eps=float("nan")), BAD), (dict(eps=float("inf")), BAD),
     (dict(beta=float("inf")), BAD), (dict(x=A + 1), BAD), (dict(u=D), BAD), (dict(u=D + 16), BAD),
     (dict(r=A + 128), BAD), (dict(u=B + 2), BAD), (dict(ps=C), BAD), (dict(qs=E + 4), BAD), (dict(qs=D + 64), BAD),
+    (dict(r=C - 8), BAD), (dict(u=C + 252), BAD), (dict(gate=D + 8, kind=1), BAD), (dict(gate=D + 4, kind=2), BAD),
     (dict(y=None, r=None, post=None, ps=None, beta=2.0), BAD),
     (dict(y=None, r=None, post=None, ps=None, gate=C, kind=1), BAD),
     (dict(y=None, r=None, post=None, ps=None, pre=None, u=None, qs=None), BAD),
@@ -94,6 +95,7 @@ BWD = dict(y=A, r=B, dr=C, du=C + (1 << 30), gate=None, kind=0, post=C, pre=C, p
     dict(pre=None, du=None, qs=None, dpre=None, dr=None), dict(dx=B + 4), dict(dy=D + 8), dict(dy=D),
     dict(kind=1, gate=C), dict(d=0), dict(dtype=9), dict(beta=float("nan")),
     dict(dpost=C), dict(dpre=E), dict(ws=E), dict(ws=D + 16), dict(kind=2, gate=E + (1 << 20), dg=E + (1 << 20)),
+    dict(post=D + 16), dict(pre=D + (1 << 30)), dict(ps=D), dict(qs=D + 64), dict(kind=2, gate=D, dg=E + (1 << 20)),
 ])
 def test_block_norm_backward_refuses(L, kw):
     v = {**BWD, **kw}
@@ -129,6 +131,18 @@ def test_clipping_refuses_bad_tables(L, ptrs, outs, numels, dtypes):
     size = L.moe_grad_workspace(len(ptrs))
     assert L.moe_clip_grad_norm(p, o, n, d, len(ptrs), 1.0, D, D + 64, size, None) == BAD
     assert L.moe_grad_scale(p, o, n, d, len(ptrs), D, 1.0, None, None) == BAD
+
+
+def test_clipping_refuses_results_and_workspaces_on_the_tensors(L):
+    p, n, d = _tables([A], [100], [0])
+    o = (ctypes.c_void_p * 1)(B)
+    size = L.moe_grad_workspace(1)
+    for norm, ws in ((A + 8, D), (B + 8, D), (D, A), (D, B - size + 8), (D, B), (D + 8, D)):
+        assert L.moe_clip_grad_norm(p, o, n, d, 1, 1.0, norm, ws, size, None) == BAD
+    for sumsq, norm, ws in ((A, None, D), (None, A + 4, D), (D, None, A + 392), (D, D + 4, C), (D, None, D)):
+        assert L.moe_grad_sumsq(p, n, d, 1, sumsq, norm, ws, size, None) == BAD
+    for sumsq, norm in ((B, D), (D, B + 396), (D, A), (D, D + 4)):
+        assert L.moe_grad_scale(p, o, n, d, 1, sumsq, 1.0, norm, None) == BAD
 
 
 def test_clipping_refuses_bad_scalars(L):
