@@ -28,12 +28,16 @@
 // grid has one cluster per tile, experts with most rows first; a running cluster takes the
 // next unstarted one over (clusterlaunchcontrol), so no cluster is left with a long tile at
 // the end, and which cluster computes a tile does not change its value.  A warp of each CTA does
-// nothing but ask (the leader's), read the answer and hand the tile on: in the producer that
-// took 2,400 cycles a tile, which the ring could not cover.
+// nothing but ask (the leader's), read the answer and hand the tile on, worked out: in the
+// producer that took 2,400 cycles a tile, which the ring could not cover.
 //
-// Bound by the tensor cores with long sums (64 experts of 6144 rows, 1408 x 2048: 1.75 ms, 1.29
-// PFLOP/s), by HBM writes with short ones (1 row: 159 us for 738 MB); between them (768 rows: 295
-// us, 0.96 PFLOP/s) loads and stores share the L2's ports: without the stores 235 us.
+// Bound by the tensor cores with long sums (64 experts of 6144 rows, 1408 x 2048: 1.78 ms, 1.27
+// PFLOP/s).  With short ones (1 row: 144 us; 160 rows: 152) by the stores' way out of the SM: a
+// line takes 3 cycles there, and every barrier, load and MMA instruction of the other warps
+// queues with them; stores that stay in L2 take as long, so it is not HBM (738 MB: 112 us).  In
+// between (768 rows: 293 us, 0.97 PFLOP/s; 254 without the stores) both count.  Readers that
+// look up four words instead of a tile number saved 15 us of the 1-row case; stores through
+// shared memory and TMA boxes of 8 rows take 220 us there.
 #pragma once
 
 #include "grouped_tc.cuh"
@@ -106,7 +110,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
   extern __shared__ uint8_t smem_raw[];
   __shared__ WgradTable tab;
   __shared__ __align__(16) uint8_t answers[kGwSlots][16];
-  __shared__ volatile int tiles[kGwSlots];
+  __shared__ int4 tiles[kGwSlots];   // part times G plus expert, 256-blocks, rows of x and dy
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* ctl = base + (size_t)kGwStages * kGwStageBytes;
@@ -177,24 +181,24 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
   __syncthreads();
 
   struct Tile {
-    int z, m, n;      // part times G plus expert; 256-column block, 256-row block of dW
+    int z, m, n;      // part times G plus expert (< 0: no tile); 256-column block, 256-row block of dW
     int row0, grows;  // the expert's rows of this part
     int kb;           // stages
   };
-  auto tile_of = [&](int tile) {
-    Tile c;
+  // a tile in four words, as the scheduling warp hands it on: a reader has one load to wait for
+  auto describe = [&](int tile) {
+    if (tile < 0) return make_int4(-1, 0, 0, 0);
     const int o = tile / (per_group * a.splits);
     int local = tile - o * (per_group * a.splits);
     const int part = local / per_group, g = tab.order[o];
     local -= part * per_group;
-    c.z = part * a.G + g;
-    c.m = local / nt;
-    c.n = local - c.m * nt;
-    c.row0 = tab.row0[g];
-    c.grows = tab.row0[g + 1] - c.row0;
-    split_rows(c.row0, c.grows, a.splits, part);
-    c.kb = (c.grows + kGwRows - 1) / kGwRows;
-    return c;
+    const int m = local / nt;
+    int row0 = tab.row0[g], rows = tab.row0[g + 1] - row0;
+    split_rows(row0, rows, a.splits, part);
+    return make_int4(part * a.G + g, m << 16 | (local - m * nt), row0, rows);   // (blocks: below 2^12)
+  };
+  auto tile_of = [&](const int4& t) {
+    return Tile{t.x, t.y >> 16, t.y & 0xffff, t.z, t.w, (t.w + kGwRows - 1) / kGwRows};
   };
   auto tile_cols = [&](int n) {   // the MMA's N: a multiple of 32
     const int left = a.N - n * kGemmBN;
@@ -208,16 +212,27 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
       if (++i == kGwSlots) { i = 0; phase ^= 1u; }
     }
   };
-  // The tile the scheduling warp hands on (one thread of each reader); -1: none left, or a wait ran out.
+  // The tile the scheduling warp hands on, to one thread of each reader or to a warp; x < 0: none
+  // left, or a wait ran out.
   auto next_tile = [&](Slot& sl) {
-    if (!mbar_wait(smem_u32(&tile_full[sl.i]), sl.phase, abort_flag, err, kErrWaitProducer)) return -1;
-    const int tile = tiles[sl.i];
-    if (tile >= -1) mbar_arrive_relaxed(smem_u32(&tile_empty[sl.i]));   // (always: the value has arrived)
+    if (!mbar_wait(smem_u32(&tile_full[sl.i]), sl.phase, abort_flag, err, kErrWaitProducer))
+      return make_int4(-1, 0, 0, 0);
+    const int4 t = tiles[sl.i];
+    if (t.x >= -1) mbar_arrive_relaxed(smem_u32(&tile_empty[sl.i]));   // (always: the value has arrived)
     sl.next();
-    return tile;
+    return t;
+  };
+  auto warp_tile = [&](Slot& sl) {
+    int4 t = make_int4(0, 0, 0, 0);
+    if (lane == 0) t = next_tile(sl);
+    t.x = __shfl_sync(0xffffffffu, t.x, 0);
+    t.y = __shfl_sync(0xffffffffu, t.y, 0);
+    t.z = __shfl_sync(0xffffffffu, t.z, 0);
+    t.w = __shfl_sync(0xffffffffu, t.w, 0);
+    return t;
   };
 
-  const int first = blockIdx.x >> 1;
+  const int4 first = describe(blockIdx.x >> 1);
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -225,7 +240,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
       uint32_t phase = 0;
       bool ok = true;
       Slot sl;
-      for (int tile = first; tile >= 0 && ok;) {
+      for (int4 tile = first; tile.x >= 0 && ok;) {
         const Tile c = tile_of(tile);
         const int a0 = c.m * kPairBM + (int)rank * 128;
         const int b0 = c.n * kGemmBN + (int)rank * (tile_cols(c.n) / 2);
@@ -264,7 +279,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
       uint32_t phase = 0;
       bool ok = true;
       Slot sl;
-      for (int tile = first; tile >= 0 && ok;) {
+      for (int4 tile = first; tile.x >= 0 && ok;) {
         const Tile c = tile_of(tile);
         const uint32_t idesc = idesc_bf16_f32(kPairBM, tile_cols(c.n)) | kIdescAMn | kIdescBMn;
         for (int kc = 0; kc < c.kb && ok; kc += kGwChunk, ++it) {
@@ -299,7 +314,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
     int stage = 0;
     uint32_t tail_phase = 0;   // a bit per stage
     Slot sl;
-    for (int tile = first; tile >= 0;) {
+    for (int4 tile = first; tile.x >= 0;) {
       const Tile c = tile_of(tile);
       const int last = (stage + c.kb + kGwStages - 1) % kGwStages;
       stage = (stage + c.kb) % kGwStages;
@@ -329,8 +344,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
         tail_phase ^= 1u << last;
       }
-      if (lane == 0) tile = next_tile(sl);
-      tile = __shfl_sync(0xffffffffu, tile, 0);
+      tile = warp_tile(sl);
     }
   } else if (warp == 3 + kGpEpiWarps) {
     // ------------------------------------------------------------------ tiles to take over
@@ -355,13 +369,14 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
         return cta < 0 ? -1 : cta >> 1;
       };
       for (int i = 0; i < kGwAhead && leader && ok; ++i) request();
-      for (int tile = first; tile >= 0;) {
+      for (int tile = 0; tile >= 0;) {
         tile = answer();
         if (ok && tile >= 0 && leader) request();
         if (!ok) break;
+        const int4 t = describe(tile);
         ok = mbar_wait(smem_u32(&tile_empty[out.i]), out.phase ^ 1u, abort_flag, err, kErrWaitProducer);
         if (!ok) break;
-        tiles[out.i] = tile;
+        tiles[out.i] = t;
         mbar_arrive(smem_u32(&tile_full[out.i]));
         out.next();
       }
@@ -379,7 +394,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
     const int half = (warp - 2) >> 2;       // which half of the tile's columns
     int it = 0;
     Slot sl;
-    for (int tile = first; tile >= 0;) {
+    for (int4 tile = first; tile.x >= 0;) {
       const Tile c = tile_of(tile);
       // this thread's column of dW, 128 of its rows; an expert without rows leaves zeros
       uint32_t s[4][32];
@@ -433,8 +448,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
           o += a.K;
         }
       }
-      if (lane == 0) tile = next_tile(sl);
-      tile = __shfl_sync(0xffffffffu, tile, 0);
+      tile = warp_tile(sl);
     }
   }
 
