@@ -16,8 +16,12 @@
 // HBM once.  CTAs are persistent: parameters stay in registers, the next row is on its way
 // to shared memory while this one is reduced (each thread copies, and later reads, its own 16
 // bytes, so nothing waits for another thread's copies), and the backward's column sums are
-// kept per CTA.  Every sum and statistic is fp32.  u and the statistic s(r) come from r before
-// it is rounded to its type (one rounding less than reading it back).
+// kept per CTA.  Rows of other widths than whole 16-byte accesses start anywhere: their accesses
+// still are the aligned ones that the row touches (SHIFT), the elements of neighbouring rows in the
+// first and the last masked; a CTA (a warp) takes rows that all start alike, so that a thread's
+// columns, its parameters and column sums stay its own.  Every sum and statistic is fp32.  u and
+// the statistic s(r) come from r before it is rounded to its type (one rounding less than reading
+// it back).
 //
 // Bound by HBM: bf16, both norms and a channel gate, forward 6.2 TB/s at 32,768 x 4096 (173 us, 0.95
 // of the copy rate) and 5.7 at 16,384 x 2048 (47 us); backward 5.3 and 5.4 (303 and 75 us), where
@@ -116,10 +120,34 @@ struct RowVec<float, 1> {
   }
 };
 
-// V consecutive fp32 parameters (weights, channel gate): 16-byte loads when V allows.
-template <int V>
-__device__ __forceinline__ void load_param(const float* p, int i, float (&f)[V]) {
-  if constexpr (V % 4 == 0) {
+// Whether columns [c, c + V) reach over the row's ends (only with SHIFT), and column c + j is inside.
+template <int V, bool SHIFT>
+__device__ __forceinline__ bool at_edge(int c, int d) { return SHIFT && (c < 0 || c + V > d); }
+__device__ __forceinline__ bool inside(int c, int d) { return c >= 0 && c < d; }
+
+// V columns of a row's result, those inside the row: `base` is the row's first element.
+template <typename T, int V, bool SHIFT>
+__device__ __forceinline__ void store_row(void* p, int64_t base, int c, int d, const float (&f)[V]) {
+  if (at_edge<V, SHIFT>(c, d)) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (inside(c + j, d)) {
+        const float one[1] = {f[j]};
+        RowVec<T, 1>::store(p, base + c + j, one);
+      }
+  } else {
+    RowVec<T, V>::store(p, base + c, f);
+  }
+}
+
+// V consecutive fp32 parameters (weights, channel gate): 16-byte loads when V allows; with SHIFT one
+// by one, 0 outside the row.
+template <int V, bool SHIFT>
+__device__ __forceinline__ void load_param(const float* p, int i, int d, float (&f)[V]) {
+  if constexpr (SHIFT) {
+#pragma unroll
+    for (int q = 0; q < V; ++q) f[q] = inside(i + q, d) ? __ldg(p + i + q) : 0.f;
+  } else if constexpr (V % 4 == 0) {
 #pragma unroll
     for (int q = 0; q < V / 4; ++q) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(p + i) + q);
@@ -131,16 +159,20 @@ __device__ __forceinline__ void load_param(const float* p, int i, float (&f)[V])
   }
 }
 
-// V consecutive fp32 values stored.
-template <int V>
-__device__ __forceinline__ void store_f32(float* p, const float (&f)[V]) {
-  if constexpr (V % 4 == 0) {
+// V consecutive fp32 values stored to columns c.. of p.
+template <int V, bool SHIFT>
+__device__ __forceinline__ void store_f32(float* p, int c, int d, const float (&f)[V]) {
+  if constexpr (SHIFT) {
+#pragma unroll
+    for (int q = 0; q < V; ++q)
+      if (inside(c + q, d)) p[c + q] = f[q];
+  } else if constexpr (V % 4 == 0) {
 #pragma unroll
     for (int q = 0; q < V / 4; ++q)
-      *(reinterpret_cast<float4*>(p) + q) = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+      *(reinterpret_cast<float4*>(p + c) + q) = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
   } else {
 #pragma unroll
-    for (int q = 0; q < V; ++q) p[q] = f[q];
+    for (int q = 0; q < V; ++q) p[c + q] = f[q];
   }
 }
 
@@ -247,7 +279,7 @@ __host__ __device__ constexpr size_t norm_ring_bytes(int streams, int nv, int th
 
 // K row streams of one thread, NV accesses each: through the ring, or (no ring) to registers: one
 // row ahead (EARLY) or when the row's turn comes.  An absent stream has a null pointer.
-template <typename T, int V, int NV, int K, bool RING, bool EARLY>
+template <typename T, int V, int NV, int K, bool RING, bool EARLY, bool SHIFT>
 struct RowStreams {
   using RV = RowVec<T, V>;
   using Raw = typename RV::Raw;
@@ -276,10 +308,18 @@ struct RowStreams {
           if (src[k])
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-              if (col(i) < d)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem + ((to * K + k) * NV + i) * pitch),
-                             "l"(static_cast<const T*>(src[k]) + row * d + col(i))
-                             : "memory");
+              if (col(i) < d) {
+                const T* from = static_cast<const T*>(src[k]) + row * d + col(i);
+                const uint32_t at = smem + ((to * K + k) * NV + i) * pitch;
+                if constexpr (SHIFT) {   // not past the tensor's end
+                  const int64_t left = ((T_ - row) * d - col(i)) * (int64_t)sizeof(T);
+                  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from),
+                               "r"(left < 16 ? (int)left : 16)
+                               : "memory");
+                } else {
+                  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+                }
+              }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     } else if constexpr (EARLY) {
@@ -311,7 +351,8 @@ struct RowStreams {
             if (col(i) < d) cur[k][i] = RV::load(src[k], row * d + col(i));
     }
   }
-  __device__ __forceinline__ void get(int k, int i, float (&f)[V]) const {
+  // Access i of stream k, columns c..; zeros outside the row.
+  __device__ __forceinline__ void get(int k, int i, int c, int d, float (&f)[V]) const {
     if constexpr (RING) {
       uint32_t x, y, z, w;
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -326,6 +367,11 @@ struct RowStreams {
     } else {
       RV::widen(cur[k][i], f);
     }
+    if (at_edge<V, SHIFT>(c, d)) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (!inside(c + j, d)) f[j] = 0.f;
+    }
   }
   __device__ __forceinline__ void next() {
     if constexpr (RING) slot = slot + 1 == kNormRing ? 0 : slot + 1;
@@ -334,30 +380,31 @@ struct RowStreams {
 
 // The columns' parameters of one thread: post weight times channel gate, and the pre weight, in
 // registers (KEEP) or read again for every row.
-template <int V, int NV, bool KEEP>
+template <int V, int NV, bool KEEP, bool SHIFT>
 struct RowParams {
   const float *w_post, *gate_ch, *w_pre;   // nullptr: ones
+  int d;
   float wq[KEEP ? NV : 1][V], wp[KEEP ? NV : 1][V];
 
   __device__ __forceinline__ void scale_of(int c, float (&w)[V]) const {
 #pragma unroll
     for (int j = 0; j < V; ++j) w[j] = 1.0f;
-    if (w_post) load_param<V>(w_post, c, w);
+    if (w_post) load_param<V, SHIFT>(w_post, c, d, w);
     if (gate_ch) {
       float gc[V];
-      load_param<V>(gate_ch, c, gc);
+      load_param<V, SHIFT>(gate_ch, c, d, gc);
 #pragma unroll
       for (int j = 0; j < V; ++j) w[j] *= gc[j];
     }
   }
   template <class C>
-  __device__ __forceinline__ void init(int d, C&& col) {
+  __device__ __forceinline__ void init(C&& col) {
     if constexpr (KEEP) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (col(i) < d) {
           scale_of(col(i), wq[i]);
-          if (w_pre) load_param<V>(w_pre, col(i), wp[i]);
+          if (w_pre) load_param<V, SHIFT>(w_pre, col(i), d, wp[i]);
         }
     }
   }
@@ -374,14 +421,13 @@ struct RowParams {
 #pragma unroll
       for (int j = 0; j < V; ++j) w[j] = wp[i][j];
     } else {
-      load_param<V>(w_pre, c, w);
+      load_param<V, SHIFT>(w_pre, c, d, w);
     }
   }
 };
 
-template <typename T, int V, int NV, int MAXT>
+template <typename T, int V, int NV, int MAXT, bool SHIFT>
 __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_kernel(BlockNormArgs a) {
-  using RV = RowVec<T, V>;
   constexpr bool kWarpRow = MAXT == 32;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[2][2][32];   // two rows' sums: a row's may still be read while the next's come
@@ -391,15 +437,18 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_kernel(B
   const int tpr = kWarpRow ? 32 : blockDim.x;
   const int64_t step = kWarpRow ? (int64_t)gridDim.x * kNormWarps : gridDim.x;
   const float inv_d = 1.0f / (float)a.d;
-  auto col = [&](int i) { return (tid + i * tpr) * V; };
   int64_t row = kWarpRow ? (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5) : blockIdx.x;
+  // elements between an aligned access and the row's start, the same for all of this thread's rows
+  const int shift = SHIFT ? (int)(row % V) * (a.d % V) % V : 0;
+  auto col = [&](int i) { return (tid + i * tpr) * V - shift; };
   constexpr bool kRing = norm_rings(V, MAXT), kEarly = !kRing && norm_keeps(MAXT);
-  RowStreams<T, V, NV, 2, kRing, kEarly> in{{a.x, a.y}};
+  RowStreams<T, V, NV, 2, kRing, kEarly, SHIFT> in{{a.x, a.y}};
   in.init(ring);
 #pragma unroll
   for (int i = 0; i < kNormRing - 1; ++i) in.ask(row + i * step, a.T, a.d, i, col);
-  RowParams<V, NV, norm_keeps(MAXT)> par{a.w_post, a.gate_kind == kGateChannel ? a.gate : nullptr, a.w_pre};
-  par.init(a.d, col);
+  RowParams<V, NV, norm_keeps(MAXT), SHIFT> par{a.w_post, a.gate_kind == kGateChannel ? a.gate : nullptr, a.w_pre,
+                                                a.d};
+  par.init(col);
   // the row's own parameter is loaded a row ahead too
   auto token_gate = [&](int64_t i) { return a.gate_kind == kGateToken && i < a.T ? __ldg(a.gate + i) : 1.0f; };
   float gt_next = token_gate(row);
@@ -415,9 +464,9 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_kernel(B
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (col(i) < a.d) {
-        in.get(0, i, r[i]);
+        in.get(0, i, col(i), a.d, r[i]);
         if (a.y) {
-          in.get(1, i, p[i]);
+          in.get(1, i, col(i), a.d, p[i]);
           vfma(ss, p[i], p[i], ss);
         }
       }
@@ -439,7 +488,7 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_kernel(B
           vmul(p[i], p[i], w);
           vmul(r[i], r[i], b);
           vfma(r[i], p[i], k, r[i]);
-          RV::store(a.r, base + col(i), r[i]);
+          store_row<T, V, SHIFT>(a.r, base, col(i), a.d, r[i]);
         }
     }
     if (a.w_pre) {
@@ -457,22 +506,25 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_kernel(B
           par.pre(i, col(i), w);
           vmul(r[i], r[i], k);
           vmul(w, w, r[i]);
-          RV::store(a.u, base + col(i), w);
+          store_row<T, V, SHIFT>(a.u, base, col(i), a.d, w);
         }
     }
   }
 }
 
 // Column sums of the warps of a CTA (one warp per row), added in order by the CTA.
-template <int V, int NV>
-__device__ __forceinline__ void cta_columns(float (&acc)[NV][V], float* sh, float* part, int d) {
+template <int V, int NV, bool SHIFT>
+__device__ __forceinline__ void cta_columns(float (&acc)[NV][V], float* sh, float* part, int d, int shift) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kWidth = NV * V * 32;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < V; ++j) sh[warp * kWidth + (lane + i * 32) * V + j] = acc[i][j];
+    for (int j = 0; j < V; ++j) {
+      const int c = (lane + i * 32) * V + j - shift;
+      if (!SHIFT || c >= 0) sh[warp * kWidth + c] = acc[i][j];
+    }
   __syncthreads();
   for (int c = threadIdx.x; c < d; c += 32 * kNormWarps) {
     float v = 0.f;
@@ -484,9 +536,8 @@ __device__ __forceinline__ void cta_columns(float (&acc)[NV][V], float* sh, floa
 
 // As block_norm_kernel; the columns' sums stay in registers over a CTA's (warp's) rows, so the
 // parameter gradients cost one [gridDim.x, d] array of partial sums each.
-template <typename T, int V, int NV, int MAXT>
+template <typename T, int V, int NV, int MAXT, bool SHIFT>
 __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_bwd_kernel(BlockNormBwdArgs a) {
-  using RV = RowVec<T, V>;
   constexpr bool kWarpRow = MAXT == 32;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[2][2][32];
@@ -496,17 +547,23 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_bwd_kern
   const int tpr = kWarpRow ? 32 : blockDim.x;
   const int64_t step = kWarpRow ? (int64_t)gridDim.x * kNormWarps : gridDim.x;
   const float inv_d = 1.0f / (float)a.d;
-  auto col = [&](int i) { return (tid + i * tpr) * V; };
   int64_t row = kWarpRow ? (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5) : blockIdx.x;
+  // elements between an aligned access and the row's start, the same for all of this thread's rows
+  const int shift = SHIFT ? (int)(row % V) * (a.d % V) % V : 0;
+  auto col = [&](int i) { return (tid + i * tpr) * V - shift; };
   enum { kR = 0, kDu = 1, kDr = 2, kY = 3 };
   constexpr bool kRing = norm_rings(V, MAXT);
-  constexpr int kHeld = kRing ? NV : 1;   // accesses whose values are held from one sum to the next
-  RowStreams<T, V, NV, 4, kRing, false> in{{a.w_pre ? a.r : nullptr, a.w_pre ? a.du : nullptr, a.dr, a.y}};
+  // values held from one sum to the next; without, they are read again behind the sum: 1024 threads
+  // have 64 registers each, 512 have 128, too few for two accesses' values beside their column sums
+  constexpr bool kHolds = kRing && !(NV == 2 && MAXT == 512);
+  constexpr int kHeld = kHolds ? NV : 1;
+  RowStreams<T, V, NV, 4, kRing, false, SHIFT> in{{a.w_pre ? a.r : nullptr, a.w_pre ? a.du : nullptr, a.dr, a.y}};
   in.init(ring);
 #pragma unroll
   for (int i = 0; i < kNormRing - 1; ++i) in.ask(row + i * step, a.T, a.d, i, col);
-  RowParams<V, NV, norm_keeps(MAXT)> par{a.w_post, a.gate_kind == kGateChannel ? a.gate : nullptr, a.w_pre};
-  par.init(a.d, col);
+  RowParams<V, NV, norm_keeps(MAXT), SHIFT> par{a.w_post, a.gate_kind == kGateChannel ? a.gate : nullptr, a.w_pre,
+                                                a.d};
+  par.init(col);
   float acc_pre[NV][V], acc_s[NV][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -525,7 +582,6 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_bwd_kern
     gt_next = own(a.gate, a.gate_kind == kGateToken, row + step);
     const int64_t base = row * a.d;
     float g[NV][V], k[V], t[V], sum[V];
-    // (without the ring the values are read again behind a sum: 1024 threads have 64 registers)
     if (a.w_pre) {
       float x[kHeld][V], u[kHeld][V];   // xh, du
       vset(sum, 0.f);
@@ -534,10 +590,10 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_bwd_kern
       for (int i = 0; i < NV; ++i)
         if (col(i) < a.d) {
           float w[V];
-          in.get(kR, i, x[kRing ? i : 0]);
-          in.get(kDu, i, u[kRing ? i : 0]);
-          vmul(x[kRing ? i : 0], x[kRing ? i : 0], k);
-          vmul(t, u[kRing ? i : 0], x[kRing ? i : 0]);
+          in.get(kR, i, col(i), a.d, x[kHolds ? i : 0]);
+          in.get(kDu, i, col(i), a.d, u[kHolds ? i : 0]);
+          vmul(x[kHolds ? i : 0], x[kHolds ? i : 0], k);
+          vmul(t, u[kHolds ? i : 0], x[kHolds ? i : 0]);
           vadd(acc_pre[i], t);
           par.pre(i, col(i), w);
           vfma(sum, t, w, sum);
@@ -549,29 +605,29 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_bwd_kern
       for (int i = 0; i < NV; ++i)
         if (col(i) < a.d) {
           float w[V];
-          if constexpr (!kRing) {
-            in.get(kR, i, x[kRing ? i : 0]);
-            in.get(kDu, i, u[kRing ? i : 0]);
-            vmul(x[kRing ? i : 0], x[kRing ? i : 0], k);
+          if constexpr (!kHolds) {
+            in.get(kR, i, col(i), a.d, x[kHolds ? i : 0]);
+            in.get(kDu, i, col(i), a.d, u[kHolds ? i : 0]);
+            vmul(x[kHolds ? i : 0], x[kHolds ? i : 0], k);
           }
-          if (a.dr) in.get(kDr, i, g[i]);
+          if (a.dr) in.get(kDr, i, col(i), a.d, g[i]);
           else vset(g[i], 0.f);
           par.pre(i, col(i), w);
-          vmul(w, w, u[kRing ? i : 0]);
+          vmul(w, w, u[kHolds ? i : 0]);
           vfma(g[i], w, k, g[i]);
-          vfma(g[i], x[kRing ? i : 0], m, g[i]);
+          vfma(g[i], x[kHolds ? i : 0], m, g[i]);
         }
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (col(i) < a.d) in.get(kDr, i, g[i]);
+        if (col(i) < a.d) in.get(kDr, i, col(i), a.d, g[i]);
     }
     vset(k, a.beta);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (col(i) < a.d) {
         vmul(t, g[i], k);
-        RV::store(a.dx, base + col(i), t);
+        store_row<T, V, SHIFT>(a.dx, base, col(i), a.d, t);
       }
     if (a.y) {
       // g becomes q without the token gate: g times post weight and channel gate
@@ -583,9 +639,9 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_bwd_kern
       for (int i = 0; i < NV; ++i)
         if (col(i) < a.d) {
           float w[V];
-          in.get(kY, i, y[kRing ? i : 0]);
-          vmul(y[kRing ? i : 0], y[kRing ? i : 0], ks);
-          vmul(t, g[i], y[kRing ? i : 0]);
+          in.get(kY, i, col(i), a.d, y[kHolds ? i : 0]);
+          vmul(y[kHolds ? i : 0], y[kHolds ? i : 0], ks);
+          vmul(t, g[i], y[kHolds ? i : 0]);
           vfma(acc_s[i], t, k, acc_s[i]);
           par.post(i, col(i), w);
           vfma(sum, t, w, sum);
@@ -603,13 +659,13 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_bwd_kern
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (col(i) < a.d) {
-          if constexpr (!kRing) {
-            in.get(kY, i, y[kRing ? i : 0]);
-            vmul(y[kRing ? i : 0], y[kRing ? i : 0], ks);
+          if constexpr (!kHolds) {
+            in.get(kY, i, col(i), a.d, y[kHolds ? i : 0]);
+            vmul(y[kHolds ? i : 0], y[kHolds ? i : 0], ks);
           }
           vmul(g[i], g[i], k);
-          vfma(g[i], y[kRing ? i : 0], m, g[i]);
-          RV::store(a.dy, base + col(i), g[i]);
+          vfma(g[i], y[kHolds ? i : 0], m, g[i]);
+          store_row<T, V, SHIFT>(a.dy, base, col(i), a.d, g[i]);
         }
     }
     in.next();
@@ -617,14 +673,14 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_bwd_kern
   const int64_t o = (int64_t)blockIdx.x * a.d;
   if constexpr (kWarpRow) {
     __shared__ float sh[kNormWarps * NV * V * 32];
-    if (a.part_pre) cta_columns<V, NV>(acc_pre, sh, a.part_pre + o, a.d);
-    if (a.part_s) cta_columns<V, NV>(acc_s, sh, a.part_s + o, a.d);
+    if (a.part_pre) cta_columns<V, NV, SHIFT>(acc_pre, sh, a.part_pre + o, a.d, shift);
+    if (a.part_s) cta_columns<V, NV, SHIFT>(acc_s, sh, a.part_s + o, a.d, shift);
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (col(i) < a.d) {
-        if (a.part_pre) store_f32<V>(a.part_pre + o + col(i), acc_pre[i]);
-        if (a.part_s) store_f32<V>(a.part_s + o + col(i), acc_s[i]);
+        if (a.part_pre) store_f32<V, SHIFT>(a.part_pre + o, col(i), a.d, acc_pre[i]);
+        if (a.part_s) store_f32<V, SHIFT>(a.part_s + o, col(i), a.d, acc_s[i]);
       }
   }
 }

@@ -7,49 +7,61 @@ using namespace moe;
 
 namespace {
 
-// the widest ring: a backward CTA of 512 threads, or a forward one of 512 with two accesses each
-constexpr size_t kNormMaxSmem = norm_ring_bytes(4, 1, 512);
-static_assert(norm_ring_bytes(2, 2, 512) <= kNormMaxSmem && norm_ring_bytes(4, 2, 256) <= kNormMaxSmem, "ring");
+// the widest ring: a backward CTA of 512 threads with two accesses each
+constexpr size_t kNormMaxSmem = norm_ring_bytes(4, 2, 512);
 
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// Call f(V, NV, MAXT, threads, rows per CTA) for rows of d elements of T: 16-byte accesses when d is a
-// multiple of their elements and every row pointer is 16-byte aligned, else one element an
-// access.  A warp per row up to 64 accesses (a CTA of one warp would leave the SM half empty, a
-// wider one waits at barriers); above, per access half a thread (forward) or one (backward,
-// whose column sums take registers), up to 1024 threads.
+// How rows are read: 16 bytes at a time, d being a whole number of them and every row and parameter
+// pointer aligned; by the aligned 16 bytes that a row touches, when the row pointers are; or one
+// element at a time.
+enum class RowRead { kWhole, kShifted, kSingle };
+
+// Call f(V, NV, MAXT, SHIFT, threads, rows per CTA) for rows of d elements of T.  A warp per row up
+// to 64 accesses (a CTA of one warp would leave the SM half empty, a wider one waits at
+// barriers); above, per access half a thread (forward) or one (backward, whose column sums take
+// registers; half a thread again past 512).
 template <typename T, bool BWD, class F>
-cudaError_t with_row_shape(int d, bool vec, F&& f) {
+cudaError_t with_row_shape(int d, RowRead read, F&& f) {
   auto threads = [](int n) { return (n + 31) / 32 * 32; };
-  if (vec) {
-    constexpr int V = 16 / sizeof(T);
-    const int n = d / V;
-    constexpr int NV = BWD ? 1 : 2;
-    if (n <= 32) return f(Int<V>{}, Int<1>{}, Int<32>{}, 32 * kNormWarps, kNormWarps);
-    if (n <= 64) return f(Int<V>{}, Int<2>{}, Int<32>{}, 32 * kNormWarps, kNormWarps);
-    if (n <= NV * 256) return f(Int<V>{}, Int<NV>{}, Int<256>{}, threads((n + NV - 1) / NV), 1);
-    if (n <= NV * 512) return f(Int<V>{}, Int<NV>{}, Int<512>{}, threads((n + NV - 1) / NV), 1);
+  constexpr int V = 16 / sizeof(T);
+  constexpr int NV = BWD ? 1 : 2;
+  auto ringed = [&](auto shift, int n) {   // n <= 1024
+    if (n <= 32) return f(Int<V>{}, Int<1>{}, Int<32>{}, shift, 32 * kNormWarps, kNormWarps);
+    if (n <= 64) return f(Int<V>{}, Int<2>{}, Int<32>{}, shift, 32 * kNormWarps, kNormWarps);
+    if (n <= NV * 256) return f(Int<V>{}, Int<NV>{}, Int<256>{}, shift, threads((n + NV - 1) / NV), 1);
     if constexpr (BWD)
-      if (n <= 1024) return f(Int<V>{}, Int<1>{}, Int<1024>{}, threads(n), 1);
+      if (n <= 512) return f(Int<V>{}, Int<1>{}, Int<512>{}, shift, threads(n), 1);
+    return f(Int<V>{}, Int<2>{}, Int<512>{}, shift, threads((n + 1) / 2), 1);
+  };
+  if (read == RowRead::kWhole) {
+    const int n = d / V;
+    if (n <= 1024) return ringed(std::false_type{}, n);
     if constexpr (V < 8)   // (kNormMaxD is 2048 accesses of 8)
-      if (n > 2048) return f(Int<V>{}, Int<4>{}, Int<1024>{}, threads((n + 3) / 4), 1);
-    return f(Int<V>{}, Int<2>{}, Int<1024>{}, threads((n + 1) / 2), 1);
+      if (n > 2048) return f(Int<V>{}, Int<4>{}, Int<1024>{}, std::false_type{}, threads((n + 3) / 4), 1);
+    return f(Int<V>{}, Int<2>{}, Int<1024>{}, std::false_type{}, threads((n + 1) / 2), 1);
   }
-  if (d <= 256) return f(Int<1>{}, Int<8>{}, Int<32>{}, 32 * kNormWarps, kNormWarps);
-  if (d <= 2048) return f(Int<1>{}, Int<8>{}, Int<256>{}, threads((d + 7) / 8), 1);
-  if (d <= 4096) return f(Int<1>{}, Int<8>{}, Int<512>{}, threads((d + 7) / 8), 1);
-  if (d <= 8192) return f(Int<1>{}, Int<8>{}, Int<1024>{}, threads((d + 7) / 8), 1);
-  return f(Int<1>{}, Int<16>{}, Int<1024>{}, threads((d + 15) / 16), 1);
+  if (read == RowRead::kShifted) {
+    const int n = (d + 2 * V - 2) / V;   // at most: V - 1 elements before the row
+    if (n <= 1024) return ringed(std::true_type{}, n);
+  }
+  constexpr std::false_type no{};
+  if (d <= 256) return f(Int<1>{}, Int<8>{}, Int<32>{}, no, 32 * kNormWarps, kNormWarps);
+  if (d <= 2048) return f(Int<1>{}, Int<8>{}, Int<256>{}, no, threads((d + 7) / 8), 1);
+  if (d <= 4096) return f(Int<1>{}, Int<8>{}, Int<512>{}, no, threads((d + 7) / 8), 1);
+  if (d <= 8192) return f(Int<1>{}, Int<8>{}, Int<1024>{}, no, threads((d + 7) / 8), 1);
+  return f(Int<1>{}, Int<16>{}, Int<1024>{}, no, threads((d + 15) / 16), 1);
 }
 
 // CTAs of a persistent kernel: as many as are resident at once (asked for once per device and
-// CTA size, which also raises the kernel's shared-memory limit), at most one per row (or eight).
+// CTA size, which also raises the kernel's shared-memory limit), at most one per row (or eight); a
+// multiple of `period` when a CTA takes several rows.
 struct NormOccupancy {
   std::atomic<int> per_sm[64][33];
 };
 cudaError_t norm_grid(const void* kernel, NormOccupancy& kept, int device, int threads, size_t smem,
-                      int rows_per_cta, int64_t T, int n_sms, int* grid) {
+                      int rows_per_cta, int period, int64_t T, int n_sms, int* grid) {
   std::atomic<int>* known = device < 64 ? &kept.per_sm[device][threads / 32] : nullptr;
   int per_sm = known ? known->load(std::memory_order_acquire) : 0;
   if (per_sm == 0) {
@@ -61,7 +73,7 @@ cudaError_t norm_grid(const void* kernel, NormOccupancy& kept, int device, int t
     if (known) known->store(per_sm, std::memory_order_release);
   }
   int64_t g = (T + rows_per_cta - 1) / rows_per_cta;
-  if (g > (int64_t)n_sms * per_sm) g = (int64_t)n_sms * per_sm;
+  if (g > (int64_t)n_sms * per_sm) g = (int64_t)n_sms * per_sm / period * period;
   *grid = (int)g;
   return cudaSuccess;
 }
@@ -88,38 +100,42 @@ moe_status check_shape(int64_t T, int32_t d, int32_t dtype, int32_t gate_kind, c
 }
 
 // rows: [T, d] buffers of the row kernel; params: [d] fp32
-bool rows_vec(int32_t d, int es, std::initializer_list<const void*> rows,
-              std::initializer_list<const void*> params) {
-  if (d % (16 / es)) return false;
+RowRead row_read(int32_t d, int es, std::initializer_list<const void*> rows,
+                 std::initializer_list<const void*> params) {
   for (const void* p : rows)
-    if (!aligned16(p)) return false;
+    if (!aligned16(p)) return RowRead::kSingle;
   for (const void* p : params)
-    if (!aligned16(p)) return false;
-  return true;
+    if (!aligned16(p)) return RowRead::kShifted;
+  return d % (16 / es) ? RowRead::kShifted : RowRead::kWhole;
 }
 
+// Rows after which a row starts at the same offset from 16 bytes again, when one CTA's have to.
+constexpr int row_period(bool shift, int v) { return shift ? v : 1; }
+
 template <typename T>
-cudaError_t launch_fwd(const BlockNormArgs& a, bool vec, int device, int n_sms, cudaStream_t st) {
-  return with_row_shape<T, false>(a.d, vec, [&](auto v, auto nv, auto maxt, int threads, int rows) {
+cudaError_t launch_fwd(const BlockNormArgs& a, RowRead read, int device, int n_sms, cudaStream_t st) {
+  return with_row_shape<T, false>(a.d, read, [&](auto v, auto nv, auto maxt, auto shift, int threads, int rows) {
     static NormOccupancy kept;
-    auto kernel = block_norm_kernel<T, v(), nv(), maxt()>;
+    auto kernel = block_norm_kernel<T, v(), nv(), maxt(), shift()>;
     const size_t smem = norm_rings(v(), maxt()) ? norm_ring_bytes(2, nv(), threads) : 0;
     int grid = 0;
-    const cudaError_t e = norm_grid((const void*)kernel, kept, device, threads, smem, rows, a.T, n_sms, &grid);
+    const cudaError_t e = norm_grid((const void*)kernel, kept, device, threads, smem, rows,
+                                    row_period(shift(), v()), a.T, n_sms, &grid);
     return e != cudaSuccess ? e : launch_pdl(kernel, dim3(grid), dim3(threads), smem, st, a);
   });
 }
 
 // *parts: the CTAs, each with its own partial sums.
 template <typename T>
-cudaError_t launch_bwd(const BlockNormBwdArgs& a, bool vec, int device, int n_sms, int* parts, cudaStream_t st) {
-  return with_row_shape<T, true>(a.d, vec, [&](auto v, auto nv, auto maxt, int threads, int rows) {
+cudaError_t launch_bwd(const BlockNormBwdArgs& a, RowRead read, int device, int n_sms, int* parts, cudaStream_t st) {
+  return with_row_shape<T, true>(a.d, read, [&](auto v, auto nv, auto maxt, auto shift, int threads, int rows) {
     static NormOccupancy kept;
-    auto kernel = block_norm_bwd_kernel<T, v(), nv(), maxt()>;
+    auto kernel = block_norm_bwd_kernel<T, v(), nv(), maxt(), shift()>;
     const size_t smem = norm_rings(v(), maxt()) ? norm_ring_bytes(4, nv(), threads) : 0;
-    const cudaError_t e = norm_grid((const void*)kernel, kept, device, threads, smem, rows, a.T, n_sms, parts);
+    const cudaError_t e = norm_grid((const void*)kernel, kept, device, threads, smem, rows,
+                                    row_period(shift(), v()), a.T, n_sms, parts);
     if (e != cudaSuccess) return e;
-    if (*parts > kNormMaxParts) *parts = kNormMaxParts;
+    if (*parts > kNormMaxParts) *parts = kNormMaxParts;   // (a multiple of every period)
     return launch_pdl(kernel, dim3(*parts), dim3(threads), smem, st, a);
   });
 }
@@ -160,11 +176,11 @@ moe_status moe_block_norm(const void* x, const void* y, const float* gate, int32
   int n_sms = 0, device = 0;
   MOE_TRY(op_device(&n_sms, &device));
   BlockNormArgs a{x, y, gate, post_weight, pre_weight, r, u, post_rstd, pre_rstd, T, d, gate_kind, beta, eps};
-  const bool vec = rows_vec(d, es, {x, y, r, u},
-                            {post_weight, pre_weight, gate_kind == kGateChannel ? gate : nullptr});
+  const RowRead read = row_read(d, es, {x, y, r, u},
+                                {post_weight, pre_weight, gate_kind == kGateChannel ? gate : nullptr});
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  MOE_CUDA((dtype == MOE_BF16 ? launch_fwd<__nv_bfloat16>(a, vec, device, n_sms, st)
-                              : launch_fwd<float>(a, vec, device, n_sms, st)));
+  MOE_CUDA((dtype == MOE_BF16 ? launch_fwd<__nv_bfloat16>(a, read, device, n_sms, st)
+                              : launch_fwd<float>(a, read, device, n_sms, st)));
   return MOE_OK;
 }
 
@@ -223,10 +239,10 @@ moe_status moe_block_norm_backward(const void* y, const void* r, const void* dr,
   float* part_s = need_s ? part + (size_t)norm_max_parts(T) * d : nullptr;
   BlockNormBwdArgs a{y, r, dr, du, gate, post_weight, pre_weight, post_rstd, pre_rstd, dx, dy,
                      gate_kind == kGateToken ? d_gate : nullptr, part_pre, part_s, T, d, gate_kind, beta};
-  const bool vec = rows_vec(d, es, {y, r, dr, du, dx, dy},
-                            {post_weight, pre_weight, channel ? gate : nullptr});
-  MOE_CUDA((dtype == MOE_BF16 ? launch_bwd<__nv_bfloat16>(a, vec, device, n_sms, &parts, st)
-                              : launch_bwd<float>(a, vec, device, n_sms, &parts, st)));
+  const RowRead read = row_read(d, es, {y, r, dr, du, dx, dy},
+                                {post_weight, pre_weight, channel ? gate : nullptr});
+  MOE_CUDA((dtype == MOE_BF16 ? launch_bwd<__nv_bfloat16>(a, read, device, n_sms, &parts, st)
+                              : launch_bwd<float>(a, read, device, n_sms, &parts, st)));
   if (part_pre || part_s) {
     NormReduceArgs ra{part_pre, part_s, parts, d, post_weight, channel ? gate : nullptr, d_pre_weight,
                       d_post_weight, channel ? d_gate : nullptr};

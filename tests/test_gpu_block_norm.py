@@ -107,6 +107,51 @@ def test_only_the_norm_before(dt, d):
     _both(77, d, DT[dt], "none", False, True, beta=1.0, with_y=False, with_dr=False)
 
 
+# rows that start anywhere within 16 bytes, enough of them that each CTA takes several
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,d", [(20001, 66), (9000, 131), (5000, 333), (4000, 511), (3001, 2050), (3000, 2044),
+                                 (2000, 4091), (1500, 5003), (1201, 8170)])
+@pytest.mark.parametrize("gate", ["channel", "token"])
+def test_many_rows_that_start_anywhere(T, d, dt, gate):
+    _both(T, d, DT[dt], gate, True, True, beta=0.75)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [77, 601, 4090])
+def test_rows_that_start_anywhere_keep_to_themselves(d, dt):
+    x, y, gt, wq, wp, dr, du = _inputs(900, d, DT[dt], "channel", True, True, seed=3)
+    want = block_norm(x, y, gate=gt, post_weight=wq, pre_weight=wp)
+    grads = block_norm_backward(want, y, dr=dr, du=du, gate=gt, post_weight=wq, pre_weight=wp)
+    # a row of NaN reaches no other row, in place either
+    for row in (0, 451, 899):
+        x2, y2 = x.clone(), y.clone()
+        x2[row] = float("nan")
+        got = block_norm(x2, y2, gate=gt, post_weight=wq, pre_weight=wp,
+                         out=BlockNorm(x2, y2, torch.empty_like(want.post_rstd), torch.empty_like(want.pre_rstd)))
+        others = torch.arange(900, device="cuda") != row
+        for a, b in zip(got, want):
+            assert torch.equal(a[others], b[others])
+        assert bool(got.r[row].isnan().all()) and bool(got.u[row].isnan().all())
+        du2 = du.clone()
+        du2[row] = float("nan")
+        g2 = block_norm_backward(want, y, dr=dr, du=du2, gate=gt, post_weight=wq, pre_weight=wp)
+        assert torch.equal(g2.dx[others], grads.dx[others]) and torch.equal(g2.dy[others], grads.dy[others])
+    # parameters and results at any element, and what lies around the rows
+    for off in (1, 2, 3):
+        p = [torch.empty(d + off, device="cuda")[off:].copy_(t) for t in (gt, wq, wp)]
+        got = block_norm(x, y, gate=p[0], post_weight=p[1], pre_weight=p[2])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        g2 = block_norm_backward(want, y, dr=dr, du=du, gate=p[0], post_weight=p[1], pre_weight=p[2])
+        assert all(torch.equal(a, b) for a, b in zip(g2, grads))
+    room = torch.full((902 * d + 16,), 7.0, dtype=DT[dt], device="cuda")
+    at = (d + 7) // 8 * 8   # 16-byte aligned, rows before and behind
+    r = room[at:at + 900 * d].view(900, d)
+    got = block_norm(x, y, gate=gt, post_weight=wq, pre_weight=wp,
+                     out=BlockNorm(r, torch.empty_like(x), want.post_rstd.clone(), want.pre_rstd.clone()))
+    assert torch.equal(got.r, want.r)
+    assert bool((room[:at] == 7).all()) and bool((room[at + 900 * d:] == 7).all())
+
+
 def test_no_gradient_of_the_stream():
     _both(300, 256, torch.bfloat16, "token", True, True, beta=2.0, with_dr=False)
 
