@@ -25,7 +25,10 @@
 //
 // Bound by HBM: bf16, both norms and a channel gate, forward 6.2 TB/s at 32,768 x 4096 (173 us, 0.95
 // of the copy rate) and 5.7 at 16,384 x 2048 (47 us); backward 5.3 and 5.4 (303 and 75 us), where
-// two chained row sums and 20 instructions a value begin to show.
+// two chained row sums and 20 instructions a value begin to show.  Odd widths are bound by those
+// instructions (1.2e8 elements of bf16, d = 2001: 208 us and 361, 4.6 and 4.0 TB/s; by single
+// elements 491 and 899), rows of 64 columns by their number (8 of 32 lanes read: 1.8 TB/s), rows
+// past 8192 columns by barriers of 1024 threads (3.4 and 1.9 TB/s).
 #pragma once
 
 #include "ptx.cuh"
@@ -264,7 +267,9 @@ __device__ __forceinline__ float row_sum(float v, float* buf) {
 }
 
 // Threads of a kernel: MAXT = 32 stands for one warp per row, eight rows a CTA; else the CTA has
-// as many threads as a row needs, at most MAXT.
+// as many threads as a row needs, at most MAXT.  The kernels' second launch bound is the CTAs that
+// are to fit an SM: without it the forward's took up to 163 registers, one CTA (bf16, d = 333: 475
+// us against 323; d = 3333: 376 against 236; 1.2e8 elements).
 constexpr int kNormWarps = 8;
 constexpr int kNormRing = 2;   // rows in shared memory: the one at work and the next
                                // (three: 2% faster at d = 4096, up to 11% slower elsewhere)
@@ -427,7 +432,7 @@ struct RowParams {
 };
 
 template <typename T, int V, int NV, int MAXT, bool SHIFT>
-__global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_kernel(BlockNormArgs a) {
+__global__ void __launch_bounds__(norm_max_threads(MAXT), V > 1 && MAXT <= 384 ? 2 : 1) block_norm_kernel(BlockNormArgs a) {
   constexpr bool kWarpRow = MAXT == 32;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[2][2][32];   // two rows' sums: a row's may still be read while the next's come
@@ -537,7 +542,7 @@ __device__ __forceinline__ void cta_columns(float (&acc)[NV][V], float* sh, floa
 // As block_norm_kernel; the columns' sums stay in registers over a CTA's (warp's) rows, so the
 // parameter gradients cost one [gridDim.x, d] array of partial sums each.
 template <typename T, int V, int NV, int MAXT, bool SHIFT>
-__global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_bwd_kernel(BlockNormBwdArgs a) {
+__global__ void __launch_bounds__(norm_max_threads(MAXT), MAXT == 160 ? 3 : MAXT == 320 ? 2 : 1) block_norm_bwd_kernel(BlockNormBwdArgs a) {
   constexpr bool kWarpRow = MAXT == 32;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[2][2][32];
@@ -553,9 +558,9 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), 1) block_norm_bwd_kern
   auto col = [&](int i) { return (tid + i * tpr) * V - shift; };
   enum { kR = 0, kDu = 1, kDr = 2, kY = 3 };
   constexpr bool kRing = norm_rings(V, MAXT);
-  // values held from one sum to the next; without, they are read again behind the sum: 1024 threads
-  // have 64 registers each, 512 have 128, too few for two accesses' values beside their column sums
-  constexpr bool kHolds = kRing && !(NV == 2 && MAXT == 512);
+  // values held from one sum to the next; without, they are read again behind the sum: there are too
+  // few registers for two accesses' values beside their column sums
+  constexpr bool kHolds = kRing && !(NV == 2 && MAXT >= 160);
   constexpr int kHeld = kHolds ? NV : 1;
   RowStreams<T, V, NV, 4, kRing, false, SHIFT> in{{a.w_pre ? a.r : nullptr, a.w_pre ? a.du : nullptr, a.dr, a.y}};
   in.init(ring);

@@ -21,7 +21,11 @@ enum class RowRead { kWhole, kShifted, kSingle };
 // Call f(V, NV, MAXT, SHIFT, threads, rows per CTA) for rows of d elements of T.  A warp per row up
 // to 64 accesses (a CTA of one warp would leave the SM half empty, a wider one waits at
 // barriers); above, per access half a thread (forward) or one (backward, whose column sums take
-// registers; half a thread again past 512).
+// registers; half a thread again past 512).  bf16 rows just past a size at which one CTA fewer
+// fits an SM are run by CTAs held to the registers of one more: backward of 2056 columns 485 us
+// -> 366 (2816: 331 against 411, so up to 320 accesses), of 5000 518 -> 402 (6000: 447 against
+// 454, so up to 640), forward of 5000 232 -> 190 (not of 4501 by single accesses at its ends:
+// 331 against 354), all of 1.2e8 elements.
 template <typename T, bool BWD, class F>
 cudaError_t with_row_shape(int d, RowRead read, F&& f) {
   auto threads = [](int n) { return (n + 31) / 32 * 32; };
@@ -31,8 +35,14 @@ cudaError_t with_row_shape(int d, RowRead read, F&& f) {
     if (n <= 32) return f(Int<V>{}, Int<1>{}, Int<32>{}, shift, 32 * kNormWarps, kNormWarps);
     if (n <= 64) return f(Int<V>{}, Int<2>{}, Int<32>{}, shift, 32 * kNormWarps, kNormWarps);
     if (n <= NV * 256) return f(Int<V>{}, Int<NV>{}, Int<256>{}, shift, threads((n + NV - 1) / NV), 1);
+    if constexpr (BWD && V == 8)
+      if (n <= 320) return f(Int<V>{}, Int<2>{}, Int<160>{}, shift, threads((n + 1) / 2), 1);
     if constexpr (BWD)
       if (n <= 512) return f(Int<V>{}, Int<1>{}, Int<512>{}, shift, threads(n), 1);
+    if constexpr (BWD && V == 8)
+      if (n <= 640) return f(Int<V>{}, Int<2>{}, Int<320>{}, shift, threads((n + 1) / 2), 1);
+    if constexpr (!BWD && V == 8 && !shift())
+      if (n <= 768) return f(Int<V>{}, Int<2>{}, Int<384>{}, shift, threads((n + 1) / 2), 1);
     return f(Int<V>{}, Int<2>{}, Int<512>{}, shift, threads((n + 1) / 2), 1);
   };
   if (read == RowRead::kWhole) {
@@ -42,7 +52,9 @@ cudaError_t with_row_shape(int d, RowRead read, F&& f) {
       if (n > 2048) return f(Int<V>{}, Int<4>{}, Int<1024>{}, std::false_type{}, threads((n + 3) / 4), 1);
     return f(Int<V>{}, Int<2>{}, Int<1024>{}, std::false_type{}, threads((n + 1) / 2), 1);
   }
-  if (read == RowRead::kShifted) {
+  // (narrow bf16 rows would be all ends: forward of 129 columns 511 us, 378 by single elements; of 257
+  // 396, 637 by single elements; 1.2e8 elements)
+  if (read == RowRead::kShifted && (V < 8 || d > 256)) {
     const int n = (d + 2 * V - 2) / V;   // at most: V - 1 elements before the row
     if (n <= 1024) return ringed(std::true_type{}, n);
   }

@@ -109,15 +109,15 @@ def test_only_the_norm_before(dt, d):
 
 # rows that start anywhere within 16 bytes, enough of them that each CTA takes several
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
-@pytest.mark.parametrize("T,d", [(20001, 66), (9000, 131), (5000, 333), (4000, 511), (3001, 2050), (3000, 2044),
-                                 (2000, 4091), (1500, 5003), (1201, 8170)])
+@pytest.mark.parametrize("T,d", [(20001, 66), (9000, 131), (7000, 257), (5000, 333), (4000, 511), (3001, 2050),
+                                 (3000, 2044), (2500, 2600), (2000, 4091), (1700, 4808), (1500, 5003), (1201, 8170)])
 @pytest.mark.parametrize("gate", ["channel", "token"])
 def test_many_rows_that_start_anywhere(T, d, dt, gate):
     _both(T, d, DT[dt], gate, True, True, beta=0.75)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
-@pytest.mark.parametrize("d", [77, 601, 4090])
+@pytest.mark.parametrize("d", [77, 257, 601, 2101, 4090, 4501])
 def test_rows_that_start_anywhere_keep_to_themselves(d, dt):
     x, y, gt, wq, wp, dr, du = _inputs(900, d, DT[dt], "channel", True, True, seed=3)
     want = block_norm(x, y, gate=gt, post_weight=wq, pre_weight=wp)
