@@ -1,6 +1,6 @@
 // grouped_warp.cuh -- the products of grouped_mm.cuh for bf16 operands that TMA cannot take (a width
 // that is no multiple of 8, a buffer off a 16-byte boundary): warp-level tensor-core products
-// (mma.sync), operands loaded element by element.
+// (mma.sync), operands read by the aligned 16 bytes that hold them and shifted in registers.
 //
 // BM x BN tiles, a warp WM x WN of it, 32 contraction values a step through two buffers in
 // shared memory (the next step's elements are on their way in registers while this one is
@@ -9,8 +9,10 @@
 // (16-byte chunks swizzled, or rows padded by 16 bytes, so that the reads do not meet in a bank).
 // wgrad adds up its accumulators in registers every kGwpChunk steps (see grouped_wgrad.cuh).
 //
-// Bound by the element-wise loads: 8 experts of 1000 rows, 1001 x 2003: mm 464 us, dgrad 358, wgrad
-// 423 (69 to 90 TFLOP/s; the FMA kernel 1210, 970, 1063).
+// 8 experts of 1000 rows, 1001 x 2003: mm 279 us, dgrad 295, wgrad 283 (109 to 115 TFLOP/s; loaded
+// element by element 465, 358, 478; the FMA kernel 1210, 970, 1063).  Bound by the traffic between
+// L1, registers and shared memory: most of a step's 64 wide loads touch eight lines each, and the
+// MMAs' operands pass shared memory twice.
 #pragma once
 
 #include "grouped_mm.cuh"
@@ -60,13 +62,53 @@ struct WarpTile {
   }
 };
 
+// Eight consecutive elements that start anywhere: the one or two aligned 16 bytes that hold them,
+// and the elements to drop from the front.
+struct WarpUnit {
+  uint4 x, y;
+  int drop;
+
+  // Elements at `at`, zeros from the `valid`-th on; nothing outside [lo, hi) is read.
+  __device__ __forceinline__ void load(const __nv_bfloat16* at, int valid, const __nv_bfloat16* lo,
+                                       const __nv_bfloat16* hi) {
+    x = y = make_uint4(0u, 0u, 0u, 0u);
+    drop = 0;
+    if (valid <= 0) return;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15u) >> 1;
+    const __nv_bfloat16* from = at - off;
+    if (valid >= 8 && from >= lo && hi - from >= (off ? 16 : 8)) {
+      x = __ldg(reinterpret_cast<const uint4*>(from));
+      if (off) y = __ldg(reinterpret_cast<const uint4*>(from) + 1);
+      drop = off;
+    } else {   // the row's end, or the buffer's
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < valid && hi - at > j)
+          w[j >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(at) + j)) << (16 * (j & 1));
+      x = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  __device__ __forceinline__ uint4 aligned() const {
+    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    uint32_t u[7], v[5];
+#pragma unroll
+    for (int j = 0; j < 7; ++j) u[j] = drop & 2 ? w[j + 1] : w[j];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) v[j] = drop & 4 ? u[j + 2] : u[j];
+    const int bits = (drop & 1) * 16;
+    return make_uint4(__funnelshift_r(v[0], v[1], bits), __funnelshift_r(v[1], v[2], bits),
+                      __funnelshift_r(v[2], v[3], bits), __funnelshift_r(v[3], v[4], bits));
+  }
+};
+
 template <int OP, int BM, int BN, int WM, int WN, int MINB>
 __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 32, MINB) grouped_warp_kernel(GroupedWarpArgs p) {
   constexpr int kThreads = (BM / WM) * (BN / WN) * 32;
   constexpr bool W = OP == kGroupedWgrad, kAMn = W, kBMn = OP != kGroupedMM;
   using TA = WarpTile<kAMn, BM>;
   using TB = WarpTile<kBMn, BN>;
-  constexpr int kA = BM * kGwpBK / kThreads, kB = BN * kGwpBK / kThreads;   // elements a thread loads
+  constexpr int kA = BM * kGwpBK / 8 / kThreads, kB = BN * kGwpBK / 8 / kThreads;   // units a thread loads
   constexpr int MI = WM / 16, NI = WN / 8;
   pdl_launch_dependents();
   pdl_wait();
@@ -81,6 +123,8 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 32, MINB) grouped_warp
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wm = warp % (BM / WM) * WM, wn = warp / (BM / WM) * WN;
   const int lda = OP == kGroupedMM ? p.K : p.N;
+  const __nv_bfloat16* a_end = p.a + (size_t)p.rows * lda;
+  const __nv_bfloat16* b_end = p.b + (W ? (size_t)p.rows * p.K : (size_t)p.G * p.N * p.K);
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
     const int g = group_of(tab, p.G, tile);
     int local = tile - tab.tile0[g], part = 0;
@@ -95,33 +139,39 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 32, MINB) grouped_warp
     const int Q = OP == kGroupedMM ? p.K : OP == kGroupedDgrad ? p.N : grows;
     const __nv_bfloat16* A = p.a + (size_t)grow0 * lda;
     const __nv_bfloat16* B = p.b + (W ? (size_t)grow0 * p.K : (size_t)g * p.N * p.K);
-    __nv_bfloat16 ra[kA], rb[kB];
-    const __nv_bfloat16 zero = __float2bfloat16_rn(0.f);
-    // consecutive threads along each operand's contiguous index
+    WarpUnit ra[kA], rb[kB];
+    // Consecutive threads along each operand's contiguous index.  Past the contraction's end
+    // both operands are zeros; past an output index' end anything, since no result has it.
     auto fetch = [&](int q0) {
 #pragma unroll
       for (int l = 0; l < kA; ++l) {
         const int i = tid + l * kThreads;
-        const int m = m0 + (kAMn ? i % BM : i / kGwpBK), q = q0 + (kAMn ? i / BM : i % kGwpBK);
-        ra[l] = m < M && q < Q ? A[kAMn ? (size_t)q * lda + m : (size_t)m * lda + q] : zero;
+        const int m = m0 + (kAMn ? i % (BM / 8) * 8 : i / (kGwpBK / 8));
+        const int q = q0 + (kAMn ? i / (BM / 8) : i % (kGwpBK / 8) * 8);
+        ra[l].load(A + (kAMn ? (size_t)q * lda + m : (size_t)m * lda + q),
+                   m >= M ? 0 : kAMn ? (q < Q ? 8 : 0) : Q - q, p.a, a_end);
       }
 #pragma unroll
       for (int l = 0; l < kB; ++l) {
         const int i = tid + l * kThreads;
-        const int n = n0 + (kBMn ? i % BN : i / kGwpBK), q = q0 + (kBMn ? i / BN : i % kGwpBK);
-        rb[l] = n < out_cols && q < Q ? B[kBMn ? (size_t)q * p.K + n : (size_t)n * p.K + q] : zero;
+        const int n = n0 + (kBMn ? i % (BN / 8) * 8 : i / (kGwpBK / 8));
+        const int q = q0 + (kBMn ? i / (BN / 8) : i % (kGwpBK / 8) * 8);
+        rb[l].load(B + (kBMn ? (size_t)q * p.K + n : (size_t)n * p.K + q),
+                   n >= out_cols ? 0 : kBMn ? (q < Q ? 8 : 0) : Q - q, p.b, b_end);
       }
     };
     auto put = [&](int buf) {
 #pragma unroll
       for (int l = 0; l < kA; ++l) {
         const int i = tid + l * kThreads;
-        As[buf][TA::at(kAMn ? i % BM : i / kGwpBK, kAMn ? i / BM : i % kGwpBK)] = ra[l];
+        const int o = kAMn ? i % (BM / 8) * 8 : i / (kGwpBK / 8), q = kAMn ? i / (BM / 8) : i % (kGwpBK / 8) * 8;
+        *reinterpret_cast<uint4*>(&As[buf][TA::at(o, q)]) = ra[l].aligned();
       }
 #pragma unroll
       for (int l = 0; l < kB; ++l) {
         const int i = tid + l * kThreads;
-        Bs[buf][TB::at(kBMn ? i % BN : i / kGwpBK, kBMn ? i / BN : i % kGwpBK)] = rb[l];
+        const int o = kBMn ? i % (BN / 8) * 8 : i / (kGwpBK / 8), q = kBMn ? i / (BN / 8) : i % (kGwpBK / 8) * 8;
+        *reinterpret_cast<uint4*>(&Bs[buf][TB::at(o, q)]) = rb[l].aligned();
       }
     };
     float acc[MI][NI][4], sum[W ? MI : 1][W ? NI : 1][4];

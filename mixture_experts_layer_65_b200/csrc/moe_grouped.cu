@@ -67,12 +67,16 @@ cudaError_t launch_simt(const GroupedSimtArgs& a, const Shape& s, int n_sms, cud
   return launch_simt_tile<OP, 32, 32, 4, 1, 4>(a, s, n_sms, st);
 }
 
-// bf16 that TMA cannot take: 64 x 64 tiles where 128 x 128 would not give every SM one.
+// bf16 that TMA cannot take: 64 x 64 tiles where 128 x 128 would not give every SM one.  Weight
+// gradients, which keep two sets of sums, have an SM's registers for one CTA of the larger tiles
+// (64 experts of 5 rows, 515 x 1027: 102 us, two that spill 131; one of 5000 rows, 777 x 1313: 189
+// against 175).
 template <int OP, int BM, int BN, int WM, int WN>
 cudaError_t launch_warp_tile(const GroupedWarpArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
   constexpr int kThreads = (BM / WM) * (BN / WN) * 32;
-  const int64_t tiles = a.splits * tiles_of<OP>(s, BM, BN), most = (int64_t)n_sms * (512 / kThreads);
-  return launch_pdl(grouped_warp_kernel<OP, BM, BN, WM, WN, 512 / kThreads>, dim3((unsigned)(tiles < most ? tiles : most)),
+  constexpr int kCtas = (OP == kGroupedWgrad && BM == 128 ? 256 : 512) / kThreads;   // of an SM
+  const int64_t tiles = a.splits * tiles_of<OP>(s, BM, BN), most = (int64_t)n_sms * kCtas;
+  return launch_pdl(grouped_warp_kernel<OP, BM, BN, WM, WN, kCtas>, dim3((unsigned)(tiles < most ? tiles : most)),
                     dim3(kThreads), 0, st, a);
 }
 template <int OP>

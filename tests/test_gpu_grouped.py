@@ -193,6 +193,21 @@ def test_unaligned_views_and_many_groups(op):
     _check(op, shift, b, c, FN[op](shift, b, c))
 
 
+# operands that start at any element, in memory whose other elements are NaN
+@pytest.mark.parametrize("off_a,off_b", [(i, (3 * i + 1) % 8) for i in range(8)])
+@pytest.mark.parametrize("n,k,counts", [(33, 35, [5, 0, 40, 1]), (77, 130, [129, 3, 64]), (700, 645, [900, 0, 531]),
+                                        (1, 9, [3]), (64, 48, [70, 2])])
+@pytest.mark.parametrize("op", ["mm", "dgrad", "wgrad"])
+def test_operands_that_start_anywhere(op, n, k, counts, off_a, off_b):
+    a, b, c = _inputs(op, counts, n, k, torch.bfloat16, seed=off_a)
+
+    def moved(t, off):
+        room = torch.full((t.numel() + 32,), float("nan"), dtype=t.dtype, device="cuda")
+        return room[8 + off:8 + off + t.numel()].view(t.shape).copy_(t)
+
+    _check(op, a, b, c, FN[op](moved(a, off_a), moved(b, off_b), c))
+
+
 @pytest.mark.parametrize("op", ["mm", "dgrad", "wgrad"])
 def test_no_rows_at_all(op):
     a, b, c = _inputs(op, [0, 0], 64, 72, torch.bfloat16)
