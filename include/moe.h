@@ -310,7 +310,7 @@ void moe_ep_destroy(moe_ep_handle* handle);
  * the last expert's are not read into any result and not written; a negative count counts as
  * 0, and rows that counts claims past `rows` are ignored.  1 <= n_groups <= 1024, rows < 2^28
  * (0 allowed), any n and k up to 2^20; bf16 products with n and k multiples of 8 and 16-byte
- * aligned buffers are read by TMA, other bf16 ones element by element.  An output may not
+ * aligned buffers run on tcgen05 through TMA, other bf16 ones at about a tenth of its rate.  An output may not
  * overlap an input.  workspace: moe_grouped_wgrad_workspace bytes of 16-byte aligned DEVICE memory
  * (0, then NULL, unless a weight gradient with few tiles and many rows is split over its rows),
  * free again when the call's work is done.  No allocation, no host synchronisation; deterministic.
