@@ -31,12 +31,13 @@ def _columns(name: str, ts, dev) -> tuple:
     model may have thousands of them."""
     try:
         good = set(map(_device, ts)) == {dev.index} and all(map(_contiguous, ts))
-        types = [DTYPES.get(t, -1) for t in map(_dtype, ts)]
+        types = list(map(DTYPES.get, map(_dtype, ts)))
     except TypeError:   # something that is no tensor
-        good, types = False, [-1]
-    if not good or -1 in types:
+        good, types = False, [None]
+    if not good or None in types:
         _refuse(name, ts, dev)
-    return array("Q", map(_address, ts)), array("q", map(_numel, ts)), array("i", types)
+    # (lists first: an array grows with every element of an iterator)
+    return array("Q", list(map(_address, ts))), array("q", list(map(_numel, ts))), array("i", types)
 
 
 def _table(grads, outs=None):
