@@ -180,8 +180,18 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 //   wgrad: A[m, q] = dy[row0 + q][m]      B[n, q] = x[row0 + q][n]   q < rows of the group
 // KS > 1: the CTA has KS such sets of threads, each with its own buffers and every KS-th step of the
 // contraction; the sets' sums meet in shared memory, added in order.
+// BM = 128: the pieces' sums wait in shared memory (each thread's own words), so that a thread gets
+// by with 128 registers and an SM holds two CTAs (4 experts of 2368 rows, 1024 x 1024: mm 598 us ->
+// 542, dgrad 593 -> 512; 16 of 500, 512 x 512, where there are few tiles for them, 114 -> 116).
+constexpr bool simt_sums_shared(int bm) { return bm == 128; }
+constexpr size_t simt_smem_bytes(int bm, int bn) {
+  return simt_sums_shared(bm) ? (size_t)bm * bn * sizeof(float) : 0;
+}
 template <int OP, int BM, int BN, int R, int V, int KS>
-__global__ void __launch_bounds__(BM * BN / (R * R) * KS, KS > 1 ? 2 : 1) grouped_simt_kernel(GroupedSimtArgs p) {
+__global__ void __launch_bounds__(BM * BN / (R * R) * KS, KS > 1 || simt_sums_shared(BM) ? 2 : 1)
+grouped_simt_kernel(GroupedSimtArgs p) {
+  constexpr bool kShared = simt_sums_shared(BM);
+  extern __shared__ float2 piece_sums[];
   constexpr int kThreads = BM * BN / (R * R);   // of a set
   constexpr int kA = BM * kGsBK / kThreads / V, kB = BN * kGsBK / kThreads / V;   // loads of a thread
   constexpr bool W = OP == kGroupedWgrad;
@@ -262,11 +272,15 @@ __global__ void __launch_bounds__(BM * BN / (R * R) * KS, KS > 1 ? 2 : 1) groupe
       }
     };
     // a thread's outputs: R / 4 runs of four rows (columns), BM / (R / 4) (BN / (R / 4)) apart
-    float2 acc[R][R / 2], sum[R][R / 2];
+    float2 acc[R][R / 2], sum[kShared ? 1 : R][R / 2];
+    bool pieces = false;   // (kShared) sums are waiting
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int j = 0; j < R / 2; ++j) acc[i][j] = sum[i][j] = make_float2(0.f, 0.f);
+      for (int j = 0; j < R / 2; ++j) {
+        acc[i][j] = make_float2(0.f, 0.f);
+        if constexpr (!kShared) sum[i][j] = make_float2(0.f, 0.f);
+      }
     constexpr int kRunM = BM / (R / 4), kRunN = BN / (R / 4);
     __syncthreads();   // the previous tile's last step, and its sums, have been read
     if (set * kGsBK < Q) {
@@ -297,10 +311,16 @@ __global__ void __launch_bounds__(BM * BN / (R * R) * KS, KS > 1 ? 2 : 1) groupe
           for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int j = 0; j < R / 2; ++j) {
-              sum[i][j].x += acc[i][j].x;
-              sum[i][j].y += acc[i][j].y;
+              if constexpr (kShared) {
+                float2& s = piece_sums[(i * (R / 2) + j) * kThreads + tid];
+                s = pieces ? make_float2(s.x + acc[i][j].x, s.y + acc[i][j].y) : acc[i][j];
+              } else {
+                sum[i][j].x += acc[i][j].x;
+                sum[i][j].y += acc[i][j].y;
+              }
               acc[i][j] = make_float2(0.f, 0.f);
             }
+          pieces = true;
         }
         if (more) {
           put(buf ^ 1);
@@ -342,7 +362,13 @@ __global__ void __launch_bounds__(BM * BN / (R * R) * KS, KS > 1 ? 2 : 1) groupe
       for (int j = 0; j < R; ++j) {
         const int n = n0 + j / 4 * kRunN + tx * 4 + j % 4;
         if (n >= out_cols) continue;
-        const float v = j & 1 ? sum[i][j / 2].y + acc[i][j / 2].y : sum[i][j / 2].x + acc[i][j / 2].x;
+        float v = j & 1 ? acc[i][j / 2].y : acc[i][j / 2].x;
+        if constexpr (!kShared) {
+          v += j & 1 ? sum[i][j / 2].y : sum[i][j / 2].x;
+        } else if (pieces) {
+          const float2 s = piece_sums[(i * (R / 2) + j / 2) * kThreads + tid];
+          v += j & 1 ? s.y : s.x;
+        }
         if constexpr (W) {
           if (Q == 0 && p.accumulate) continue;   // nothing to add: not touched
           float* o = static_cast<float*>(p.out) + (((size_t)part * p.G + g) * p.N + m) * p.K + n;

@@ -51,9 +51,19 @@ int64_t tiles_of(const Shape& s, int bm, int bn) {
 template <int OP, int BM, int BN, int R, int V, int KS>
 cudaError_t launch_simt_tile(const GroupedSimtArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
   constexpr int kThreads = BM * BN / (R * R) * KS;
-  const int64_t tiles = a.splits * tiles_of<OP>(s, BM, BN), most = (int64_t)n_sms * (1024 / kThreads);
-  return launch_pdl(grouped_simt_kernel<OP, BM, BN, R, V, KS>, dim3((unsigned)(tiles < most ? tiles : most)),
-                    dim3(kThreads), 0, st, a);
+  constexpr size_t kSmem = simt_smem_bytes(BM, BN);
+  const auto kernel = grouped_simt_kernel<OP, BM, BN, R, V, KS>;
+  const int64_t tiles = a.splits * tiles_of<OP>(s, BM, BN), most = (int64_t)n_sms * ((kSmem ? 512 : 1024) / kThreads);
+  if constexpr (kSmem > 0) {   // (once per device)
+    static std::atomic<bool> set[64];
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess && !(device < 64 && set[device].load(std::memory_order_acquire)))
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    if (device < 64) set[device].store(true, std::memory_order_release);
+  }
+  return launch_pdl(kernel, dim3((unsigned)(tiles < most ? tiles : most)), dim3(kThreads), kSmem, st, a);
 }
 template <int OP>
 cudaError_t launch_simt(const GroupedSimtArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
