@@ -149,16 +149,21 @@ class MoEBlockGrads(NamedTuple):
     d_w_up: torch.Tensor | None
     d_w_down: torch.Tensor | None
     grad_norm: torch.Tensor | None       # [1] fp32, before clipping (max_norm given)
+    inputs: tuple = ()                   # names of the fields above that are no parameter's gradient
 
     def parameters(self) -> list:
-        """The parameters' gradients that there are."""
-        return [t for t in self[2:11] if t is not None]
+        """The parameters' gradients that there are, which `max_norm` clips.  A gradient that is
+        no parameter's (`inputs`: d_gate when the gate was given to the call, a value per token
+        among them; d_bias of a layer without a logit_bias) keeps its place in the list as a
+        tensor of no elements: it neither counts in the norm nor is scaled."""
+        return [t[:0] if name in self.inputs else t
+                for name, t in zip(self._fields[2:11], self[2:11]) if t is not None]
 
 
 class MoEBlock:
     """r = beta x + gate * norm(FFN(norm(x))): a MoELayer (its experts without its own residual)
     between the norms.  pre_weight [d], optional post_weight [d] and gate ([d], or [T, 1] given to
-    each call) are fp32.
+    each call) are fp32.  The block's own gate is a parameter; one given to a call is an input.
 
     In a stack, `next_weight` of one block's forward is the next block's pre_weight: the step
     between two blocks is then one kernel, and its norm goes to the next forward as `norm_in`
@@ -193,7 +198,8 @@ class MoEBlock:
                  max_norm: float | None = None, stream: torch.cuda.Stream | None = None) -> MoEBlockGrads:
         """Gradients of sum(dr r) + sum(du u_next) + d_aux aux after `forward` (the layer's last
         one; the same gate, next_weight and whether norm_in was given).  max_norm: the parameters'
-        gradients are clipped to it together, and their norm before is returned."""
+        gradients (`MoEBlockGrads.parameters`) are clipped to it together, and their norm before
+        is returned; dx, du and the gradient of a gate given to the call stay as they are."""
         after = block_norm_backward(out.norm_out, out.layer.h, dr=dr, du=du,
                                     gate=self.gate if gate is None else gate, post_weight=self.post_weight,
                                     pre_weight=next_weight, beta=self.beta, stream=stream)
@@ -204,7 +210,10 @@ class MoEBlock:
             before = block_norm_backward(out.norm_in, None, dr=after.dx, du=d_in, pre_weight=self.pre_weight,
                                          stream=stream)
             dx, d_pre, d_in = before.dx, before.d_pre_weight, None
-        g = MoEBlockGrads(dx, d_in, after.d_gate, after.d_post_weight, d_pre, after.d_pre_weight, *rest, None)
+        # (one value per token is an input whoever holds it)
+        own_gate = (gate is None or gate is self.gate) and (self.gate is None or self.gate.dim() == 1)
+        inputs = (() if own_gate else ("d_gate",)) + (() if self.layer.has_bias else ("d_bias",))
+        g = MoEBlockGrads(dx, d_in, after.d_gate, after.d_post_weight, d_pre, after.d_pre_weight, *rest, None, inputs)
         if max_norm is not None:
             g = g._replace(grad_norm=clip_grad_norm(g.parameters(), max_norm, stream=stream))
         return g

@@ -56,6 +56,7 @@ class MoELayer:
         self.top_k, self.inter, self.alpha1 = top_k, inter, alpha1
         self.dtype = dtype
         self.torch_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self.has_bias = logit_bias is not None
         self.device = centroids.device
         for t in (centroids, w_gate, w_up, w_down):
             if not t.is_cuda or not t.is_contiguous() or t.dtype != self.torch_dtype:
