@@ -95,6 +95,36 @@ __device__ __forceinline__ int clc_answer(uint32_t answer) {
   return ok ? static_cast<int>(x) : -1;
 }
 
+// A scheduling warp's way through the grid: `ahead` requests open at a time until one is refused,
+// every tile granted handed on, -1 behind the last.  A refusal does not mean that the requests made
+// after it are refused too (a waiting kernel of higher priority is a reason to refuse, and may
+// be gone by then): the open ones' answers are tiles like the others, whose clusters will not
+// start any more.  No request follows an observed refusal (the instruction forbids it); clusters still
+// unstarted then start by themselves.  ask(), answer(tile) and hand(tile) return false when a wait
+// ran out.
+template <class Ask, class Answer, class Hand>
+__host__ __device__ __forceinline__ bool take_tiles_over(int ahead, Ask&& ask, Answer&& answer, Hand&& hand) {
+  int open = 0;
+  bool refused = false;
+  for (; open < ahead; ++open)
+    if (!ask()) return false;
+  while (open > 0) {
+    int tile = -1;
+    if (!answer(tile)) return false;
+    --open;
+    if (tile < 0) {
+      refused = true;
+      continue;
+    }
+    if (!refused) {
+      if (!ask()) return false;
+      ++open;
+    }
+    if (!hand(tile)) return false;
+  }
+  return hand(-1);
+}
+
 // Arrive on the peer's barrier without ordering anything (it guards only what the barrier
 // itself counts).
 __device__ __forceinline__ void mbar_arrive_expect_tx_peer(uint32_t cluster_addr, uint32_t bytes) {
@@ -349,39 +379,36 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
   } else if (warp == 3 + kGpEpiWarps) {
     // ------------------------------------------------------------------ tiles to take over
     if (lane == 0) {
-      bool ok = true;
       Slot ask, got, out;
-      auto request = [&] {   // (leader) ask for one more tile
-        ok = mbar_wait_cluster(smem_u32(&next_empty[ask.i]), ask.phase ^ 1u, abort_flag, err, kErrWaitProducer);
-        if (!ok) return;
+      auto request = [&] {   // (the leader's) ask for one more tile
+        if (!leader) return true;
+        if (!mbar_wait_cluster(smem_u32(&next_empty[ask.i]), ask.phase ^ 1u, abort_flag, err, kErrWaitProducer))
+          return false;
         mbar_arrive_expect_tx(smem_u32(&next_full[ask.i]), 16);
         mbar_arrive_expect_tx_peer(mapa_shared(smem_u32(&next_full[ask.i]), 1), 16);
         clc_try_cancel(smem_u32(answers[ask.i]), smem_u32(&next_full[ask.i]));
         ask.next();
+        return true;
       };
-      auto answer = [&] {   // the next answer: a tile or -1
-        ok = mbar_wait_cluster(smem_u32(&next_full[got.i]), got.phase, abort_flag, err, kErrWaitProducer);
-        if (!ok) return -1;
+      auto answer = [&](int& tile) {
+        if (!mbar_wait_cluster(smem_u32(&next_full[got.i]), got.phase, abort_flag, err, kErrWaitProducer))
+          return false;
         const int cta = clc_answer(smem_u32(answers[got.i]));
         fence_proxy_async_shared();   // read before the next answer is written
         if (!leader) mbar_arrive_cluster(mapa_shared(smem_u32(&next_empty[got.i]), 0));
         got.next();
-        return cta < 0 ? -1 : cta >> 1;
+        tile = cta < 0 ? -1 : cta >> 1;
+        return true;
       };
-      for (int i = 0; i < kGwAhead && leader && ok; ++i) request();
-      for (int tile = 0; tile >= 0;) {
-        tile = answer();
-        if (ok && tile >= 0 && leader) request();
-        if (!ok) break;
+      auto hand = [&](int tile) {
         const int4 t = describe(tile);
-        ok = mbar_wait(smem_u32(&tile_empty[out.i]), out.phase ^ 1u, abort_flag, err, kErrWaitProducer);
-        if (!ok) break;
+        if (!mbar_wait(smem_u32(&tile_empty[out.i]), out.phase ^ 1u, abort_flag, err, kErrWaitProducer)) return false;
         tiles[out.i] = t;
         mbar_arrive(smem_u32(&tile_full[out.i]));
         out.next();
-      }
-      // the answers to the requests that were still open when none was left
-      for (int i = 1; i < kGwAhead && ok; ++i) answer();
+        return true;
+      };
+      const bool ok = take_tiles_over(kGwAhead, request, answer, hand);
       if (!ok) {   // gave up: let the answers in flight land
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
