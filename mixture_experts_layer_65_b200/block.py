@@ -184,7 +184,7 @@ class MoEBlock:
             norm_in = block_norm(x, pre_weight=self.pre_weight, eps=self.eps, stream=stream)
         elif norm_in.u is None:
             raise ValueError("norm_in has no u: give the earlier block this block's pre_weight as next_weight")
-        with on_stream(x.device, stream):
+        with on_stream(x.device, stream, (norm_in.u,)):
             out = self.layer.forward_branch(norm_in.u)
         norm_out = block_norm(x, out.h, gate=self.gate if gate is None else gate, post_weight=self.post_weight,
                               pre_weight=next_weight, beta=self.beta, eps=self.eps, stream=stream)
@@ -203,7 +203,7 @@ class MoEBlock:
         after = block_norm_backward(out.norm_out, out.layer.h, dr=dr, du=du,
                                     gate=self.gate if gate is None else gate, post_weight=self.post_weight,
                                     pre_weight=next_weight, beta=self.beta, stream=stream)
-        with on_stream(out.r.device, stream):
+        with on_stream(out.r.device, stream, (out.norm_in.u, *out.layer)):
             d_in, *rest = self.layer.backward_branch(out.norm_in.u, out.layer, after.dy, d_aux, weights)
         dx, d_pre = after.dx, None
         if not norm_in_given:
