@@ -14,6 +14,7 @@ import numpy as np
 import torch
 
 from . import _lib
+from ._call import on_stream
 from ._lib import MoeCfg, check, lib
 
 
@@ -130,7 +131,8 @@ class MoELayer:
 
     def forward(self, u: torch.Tensor, out: MoEOutput | None = None,
                 stream: torch.cuda.Stream | None = None) -> MoEOutput:
-        """Enqueue one forward pass on `stream` (default: the current stream)."""
+        """Enqueue one forward pass on `stream` (default: the current stream).  The inputs may be
+        dropped once the call has returned; what it allocates belongs to `stream`."""
         return self._forward(lib().moe_forward, u, out, stream)
 
     def forward_branch(self, u: torch.Tensor, out: MoEOutput | None = None,
@@ -141,14 +143,25 @@ class MoELayer:
 
     def _forward(self, call, u, out, stream) -> MoEOutput:
         self._check_device_tensor("u", u, (self.T, self.d), self.torch_dtype)
-        if out is None:
-            out = self.alloc_outputs()
-        else:
+        if out is not None:
             self._check_outputs(out)
-        s = stream or torch.cuda.current_stream(self.device)
-        check(call(self._h, _ptr(u), _ptr(out.h), _ptr(out.topk_idx), _ptr(out.topk_w),
-                   _ptr(out.expert_counts), _ptr(out.aux_loss), s.cuda_stream))
+        given = out
+        with on_stream(self.device, stream, (u, *(given or ()))) as s:
+            if out is None:
+                out = self.alloc_outputs()
+            check(call(self._h, _ptr(u), _ptr(out.h), _ptr(out.topk_idx), _ptr(out.topk_w),
+                       _ptr(out.expert_counts), _ptr(out.aux_loss), s))
+        if given is None:
+            self._share(stream, out)
         return out
+
+    def _share(self, stream, made) -> None:
+        """What a call allocated on `stream` is read on the caller's stream as well: its memory is
+        not handed out while either still uses it."""
+        if stream is not None and stream != torch.cuda.current_stream(self.device):
+            for t in made:
+                if t is not None:
+                    t.record_stream(torch.cuda.current_stream(self.device))
 
     __call__ = forward
 
@@ -229,19 +242,20 @@ class MoELayer:
         self._check_device_tensor("dh", dh, (self.T, self.d), self.torch_dtype)
         self._check_outputs(out)
         dev = self.device
-        du = torch.empty(self.T, self.d, dtype=self.torch_dtype, device=dev)
-        d_cen = torch.empty(self.n_routed, self.d, dtype=torch.float32, device=dev)
-        d_bias = torch.empty(self.n_routed, dtype=torch.float32, device=dev)
-        G = self.n_shared + self.n_routed
-        dwg = dwu = dwd = None
-        if weights:
-            dwg = torch.empty(G, self.inter, self.d, dtype=torch.float32, device=dev)
-            dwu = torch.empty(G, self.inter, self.d, dtype=torch.float32, device=dev)
-            dwd = torch.empty(G, self.d, self.inter, dtype=torch.float32, device=dev)
-        s = stream or torch.cuda.current_stream(dev)
-        check(call(self._h, _ptr(u), _ptr(out.topk_idx), _ptr(out.topk_w), _ptr(out.expert_counts),
-                   _ptr(dh), float(d_aux), _ptr(du), _ptr(d_cen), _ptr(d_bias), _ptr(dwg), _ptr(dwu),
-                   _ptr(dwd), s.cuda_stream))
+        with on_stream(dev, stream, (u, *out, dh)) as s:
+            du = torch.empty(self.T, self.d, dtype=self.torch_dtype, device=dev)
+            d_cen = torch.empty(self.n_routed, self.d, dtype=torch.float32, device=dev)
+            d_bias = torch.empty(self.n_routed, dtype=torch.float32, device=dev)
+            G = self.n_shared + self.n_routed
+            dwg = dwu = dwd = None
+            if weights:
+                dwg = torch.empty(G, self.inter, self.d, dtype=torch.float32, device=dev)
+                dwu = torch.empty(G, self.inter, self.d, dtype=torch.float32, device=dev)
+                dwd = torch.empty(G, self.d, self.inter, dtype=torch.float32, device=dev)
+            check(call(self._h, _ptr(u), _ptr(out.topk_idx), _ptr(out.topk_w), _ptr(out.expert_counts),
+                       _ptr(dh), float(d_aux), _ptr(du), _ptr(d_cen), _ptr(d_bias), _ptr(dwg), _ptr(dwu),
+                       _ptr(dwd), s))
+        self._share(stream, (du, d_cen, d_bias, dwg, dwu, dwd))
         return du, d_cen, d_bias, dwg, dwu, dwd
 
     DEBUG_BUFFERS = {"slot_row": 0, "xp": 1, "hr": 2, "yr": 3, "hs": 4, "ys": 5, "grp_row": 6,

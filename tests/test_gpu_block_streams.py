@@ -39,6 +39,7 @@ def test_inputs_of_a_delayed_stream_may_be_dropped():
 
     out = blk(x)
     want = [out.r.clone(), *(t.clone() for t in blk.backward(out, dr) if t is not None and torch.is_tensor(t))]
+    _take(_sizes([out.r, out.norm_in.pre_rstd, *out.layer]))   # (a kernel's first launch may wait for the GPU)
     del out
     # forward on the side stream, its norm_in from this one
     norm_in = block_norm(x, pre_weight=p)
