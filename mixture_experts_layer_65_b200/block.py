@@ -179,11 +179,13 @@ class MoEBlock:
                 next_weight: torch.Tensor | None = None,
                 stream: torch.cuda.Stream | None = None) -> MoEBlockOutput:
         """`gate` replaces the block's own for this call; norm_in: the norm of x, computed by the
-        block before (its r is x)."""
+        block before (its r is x itself)."""
         if norm_in is None:
             norm_in = block_norm(x, pre_weight=self.pre_weight, eps=self.eps, stream=stream)
         elif norm_in.u is None:
             raise ValueError("norm_in has no u: give the earlier block this block's pre_weight as next_weight")
+        elif norm_in.r.data_ptr() != x.data_ptr() or norm_in.r.shape != x.shape:
+            raise ValueError("norm_in is the norm of another tensor: its r must be x")
         with on_stream(x.device, stream, (norm_in.u,)):
             out = self.layer.forward_branch(norm_in.u)
         norm_out = block_norm(x, out.h, gate=self.gate if gate is None else gate, post_weight=self.post_weight,

@@ -1,5 +1,6 @@
 """What a MoEBlock's layer reads is recorded on the stream it runs on (CPU only: the norms and the
 layer are stand-ins, the stream one that notes what it was given)."""
+import pytest
 import torch
 
 from mixture_experts_layer_65_b200 import block
@@ -58,3 +59,13 @@ def test_the_layers_inputs_are_recorded(monkeypatch):
     given = blk(x, norm_in=norm(x))
     blk.backward(given, x, norm_in_given=True)
     assert not Noted.open
+
+
+def test_a_norm_of_another_tensor_is_refused(monkeypatch):
+    monkeypatch.setattr(block, "block_norm", lambda *a, **kw: pytest.fail("ran"))
+    monkeypatch.setattr(block, "on_stream", Noted)
+    blk = MoEBlock(Layer(), torch.ones(D))
+    x, other = torch.zeros(T, D), torch.zeros(T, D)
+    for r in (other, x[1:], x[:3]):
+        with pytest.raises(ValueError, match="must be x"):
+            blk(x, norm_in=BlockNorm(r, torch.zeros(T, D), None, torch.zeros(T)))
