@@ -81,8 +81,8 @@ _SIGS = {
                                                ctypes.c_size_t, _P]),
     "moe_grad_workspace": (ctypes.c_size_t, [_I32]),
     "moe_grad_sumsq": (ctypes.c_int, [_P, _P, _P, _I32, _P, _P, _P, ctypes.c_size_t, _P]),
-    "moe_grad_scale": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, ctypes.c_float, _P, _P]),
-    "moe_clip_grad_norm": (ctypes.c_int, [_P, _P, _P, _P, _I32, ctypes.c_float, _P, _P,
+    "moe_grad_scale": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, ctypes.c_double, _P, _P]),
+    "moe_clip_grad_norm": (ctypes.c_int, [_P, _P, _P, _P, _I32, ctypes.c_double, _P, _P,
                                           ctypes.c_size_t, _P]),
     "moe_kernels_per_forward": (ctypes.c_int32, [_P]),
     "moe_device_bytes": (ctypes.c_size_t, [_P]),

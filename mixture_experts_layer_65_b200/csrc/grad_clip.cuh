@@ -156,25 +156,36 @@ grad_sumsq_total_kernel(const double* partial, int n, double* sumsq, float* norm
   }
 }
 
-__device__ __forceinline__ uint4 scale_16(const uint4& v, float c, __nv_bfloat16) {
+// The coefficient as the sum of two fp32 values: 48 of its bits, so that a scaled gradient is
+// rounded once (with an fp32 coefficient twice: up to a whole step of fp32 off, and the norm
+// after clipping off by the coefficient's rounding).  It costs a multiplication, which HBM hides.
+struct ClipCoef {
+  float hi, lo;
+};
+__device__ __forceinline__ float scaled(float f, const ClipCoef& c) {
+  // (lo is 0 for the coefficients 1, when f may be infinite, and 0)
+  return c.lo == 0.f ? f * c.hi : fmaf(f, c.hi, f * c.lo);
+}
+
+__device__ __forceinline__ uint4 scale_16(const uint4& v, const ClipCoef& c, __nv_bfloat16) {
   float f[8];
   bf16x8_to_f32(v, f);
-  return make_uint4(pack_bf16x2(f[0] * c, f[1] * c), pack_bf16x2(f[2] * c, f[3] * c),
-                    pack_bf16x2(f[4] * c, f[5] * c), pack_bf16x2(f[6] * c, f[7] * c));
+  return make_uint4(pack_bf16x2(scaled(f[0], c), scaled(f[1], c)), pack_bf16x2(scaled(f[2], c), scaled(f[3], c)),
+                    pack_bf16x2(scaled(f[4], c), scaled(f[5], c)), pack_bf16x2(scaled(f[6], c), scaled(f[7], c)));
 }
-__device__ __forceinline__ uint4 scale_16(const uint4& v, float c, float) {
-  return make_uint4(__float_as_uint(__uint_as_float(v.x) * c), __float_as_uint(__uint_as_float(v.y) * c),
-                    __float_as_uint(__uint_as_float(v.z) * c), __float_as_uint(__uint_as_float(v.w) * c));
+__device__ __forceinline__ uint4 scale_16(const uint4& v, const ClipCoef& c, float) {
+  return make_uint4(__float_as_uint(scaled(__uint_as_float(v.x), c)), __float_as_uint(scaled(__uint_as_float(v.y), c)),
+                    __float_as_uint(scaled(__uint_as_float(v.z), c)), __float_as_uint(scaled(__uint_as_float(v.w), c)));
 }
 
 // dst = c src over n elements; 16-byte accesses where both sides have the same offset from a
 // 16-byte boundary.  src and dst are the same buffer or do not overlap.
 template <typename T>
-__device__ __forceinline__ void chunk_scale(const T* src, T* dst, int n, float c) {
+__device__ __forceinline__ void chunk_scale(const T* src, T* dst, int n, const ClipCoef& c) {
   constexpr int V = 16 / sizeof(T);
   const int tid = threadIdx.x;
   auto one = [&](int i) {
-    const float f = clip_load1(src + i) * c;
+    const float f = scaled(clip_load1(src + i), c);
     if constexpr (sizeof(T) == 2) dst[i] = __float2bfloat16_rn(f);
     else dst[i] = f;
   };
@@ -204,8 +215,11 @@ __device__ __forceinline__ void chunk_scale(const T* src, T* dst, int n, float c
 
 // The coefficient: 1 when the norm is within max_norm or not finite (the caller sees the norm
 // and skips the step; a NaN that spread to every gradient could not be told from its source).
-__device__ __forceinline__ float clip_coef(double norm, double max_norm) {
-  return norm > max_norm && norm < __longlong_as_double(0x7ff0000000000000LL) ? (float)(max_norm / norm) : 1.0f;
+__device__ __forceinline__ ClipCoef clip_coef(double norm, double max_norm) {
+  if (!(norm > max_norm && norm < __longlong_as_double(0x7ff0000000000000LL))) return ClipCoef{1.0f, 0.0f};
+  const double c = max_norm / norm;
+  const float hi = (float)c;
+  return ClipCoef{hi, (float)(c - (double)hi)};
 }
 
 template <int N>
@@ -215,13 +229,13 @@ grad_scale_kernel(const __grid_constant__ ClipTable<N> t, ClipScaleArgs a) {
   pdl_wait();
   const double norm = sqrt(total_of(a.sumsq, a.n_sums));
   if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
-  const float coef = clip_coef(norm, a.max_norm);
+  const ClipCoef coef = clip_coef(norm, a.max_norm);
   const int chunks = t.chunk0[t.n_tensors];
   // last chunks first: they were read last and may still be in L2
   for (int k = blockIdx.x; k < chunks; k += gridDim.x) {
     const int c = chunks - 1 - k;
     const int i = clip_tensor(t, c);
-    if (coef == 1.0f && t.e[i].src == t.e[i].dst) continue;   // in place and nothing to scale
+    if (coef.hi == 1.0f && coef.lo == 0.0f && t.e[i].src == t.e[i].dst) continue;   // in place and nothing to scale
     const int64_t off = (int64_t)(c - t.chunk0[i]) * kClipChunk;
     const int64_t left = t.e[i].n - off;
     const int n = left < kClipChunk ? (int)left : kClipChunk;

@@ -167,16 +167,16 @@ moe_status moe_grad_sumsq(const void* const* grads, const int64_t* numels, const
 }
 
 moe_status moe_grad_scale(const void* const* grads, void* const* outs, const int64_t* numels,
-                          const int32_t* dtypes, int32_t n_tensors, const double* sumsq, float max_norm,
+                          const int32_t* dtypes, int32_t n_tensors, const double* sumsq, double max_norm,
                           float* norm, moe_stream_t stream) {
   if (n_tensors > 0 && !outs) return fail(MOE_ERR_INVALID_ARG, "a table pointer is NULL");
   MOE_TRY(check_tensors(grads, outs, numels, dtypes, n_tensors, {{sumsq, 8}, {norm, 4}}));
   if (!sumsq) return fail(MOE_ERR_INVALID_ARG, "sumsq is NULL");
-  if (!(max_norm >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "max_norm must not be negative or NaN");
+  if (!(max_norm >= 0.0)) return fail(MOE_ERR_INVALID_ARG, "max_norm must not be negative or NaN");
   int n_sms = 0;
   MOE_TRY(op_device(&n_sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  ClipScaleArgs a{sumsq, 1, (double)max_norm, norm};
+  ClipScaleArgs a{sumsq, 1, max_norm, norm};
   const int k = non_empty(numels, n_tensors);
   if (k == 0) {
     if (norm) MOE_CUDA(launch_pdl(grad_sumsq_total_kernel, dim3(1), dim3(kClipThreads), 0, st, sumsq, 1,
@@ -189,13 +189,13 @@ moe_status moe_grad_scale(const void* const* grads, void* const* outs, const int
 }
 
 moe_status moe_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels,
-                              const int32_t* dtypes, int32_t n_tensors, float max_norm, float* norm,
+                              const int32_t* dtypes, int32_t n_tensors, double max_norm, float* norm,
                               void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   if (n_tensors > 0 && !outs) return fail(MOE_ERR_INVALID_ARG, "a table pointer is NULL");
   MOE_TRY(check_tensors(grads, outs, numels, dtypes, n_tensors,
                         {{norm, 4}, {workspace, moe_grad_workspace(n_tensors)}}));
   if (!norm) return fail(MOE_ERR_INVALID_ARG, "norm is NULL");
-  if (!(max_norm >= 0.0f)) return fail(MOE_ERR_INVALID_ARG, "max_norm must not be negative or NaN");
+  if (!(max_norm >= 0.0)) return fail(MOE_ERR_INVALID_ARG, "max_norm must not be negative or NaN");
   MOE_TRY(check_workspace(workspace, workspace_bytes, n_tensors));
   int n_sms = 0, sums = 0;
   MOE_TRY(op_device(&n_sms));
@@ -209,11 +209,11 @@ moe_status moe_clip_grad_norm(const void* const* grads, void* const* outs, const
   if (k <= kClipTableSmall) {
     MOE_TRY(sumsq_launches<kClipTableSmall>(grads, numels, dtypes, n_tensors, partial, &sums, n_sms, st));
     return scale_launches<kClipTableSmall>(grads, outs, numels, dtypes, n_tensors,
-                                           ClipScaleArgs{partial, sums, (double)max_norm, norm}, n_sms, st);
+                                           ClipScaleArgs{partial, sums, max_norm, norm}, n_sms, st);
   }
   MOE_TRY(sumsq_launches<kClipTable>(grads, numels, dtypes, n_tensors, partial, &sums, n_sms, st));
   return scale_launches<kClipTable>(grads, outs, numels, dtypes, n_tensors,
-                                    ClipScaleArgs{partial, sums, (double)max_norm, norm}, n_sms, st);
+                                    ClipScaleArgs{partial, sums, max_norm, norm}, n_sms, st);
 }
 
 }  // extern "C"

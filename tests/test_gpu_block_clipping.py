@@ -53,7 +53,7 @@ def test_the_norm_is_the_parameters(kind, zipf):
     scaled += [n for n in ("d_gate", "d_bias") if n not in kept]
     for n in kept:
         assert torch.equal(getattr(got, n), getattr(raw, n)), n
-    for n in scaled:   # the coefficient and the product, each rounded to fp32; max_norm too
+    for n in scaled:   # at most the coefficient, the product and max_norm rounded to fp32
         ref = getattr(raw, n).double() * 0.25
         assert bool(((getattr(got, n).double() - ref).abs() <= 3.01 * R.E * ref.abs() + 1e-44).all()), n
     layer.device_status()
