@@ -159,33 +159,44 @@ grad_sumsq_total_kernel(const double* partial, int n, double* sumsq, float* norm
 // The coefficient as the sum of two fp32 values: 48 of its bits, so that a scaled gradient is
 // rounded once (with an fp32 coefficient twice: up to a whole step of fp32 off, and the norm
 // after clipping off by the coefficient's rounding).  It costs a multiplication, which HBM hides.
-struct ClipCoef {
-  float hi, lo;
+// A coefficient below 2^-100, whose low part fp32 would lose (below 2^-126 the high one too, while the
+// gradients that made so large a norm may scale to ordinary values), multiplies in 64 bits.
+// (One form per launch, not per value: 600 MB of bf16 into others 399 us with the choice in the loop,
+// 391 without.)
+struct ScaleFp32 {   // 1, when f may be infinite, and values that fp32 has
+  float c;
+  __device__ __forceinline__ float operator()(float f) const { return f * c; }
 };
-__device__ __forceinline__ float scaled(float f, const ClipCoef& c) {
-  // (lo is 0 for the coefficients 1, when f may be infinite, and 0)
-  return c.lo == 0.f ? f * c.hi : fmaf(f, c.hi, f * c.lo);
-}
+struct ScaleTwoFp32 {
+  float hi, lo;
+  __device__ __forceinline__ float operator()(float f) const { return fmaf(f, hi, f * lo); }
+};
+struct ScaleFp64 {
+  double c;
+  __device__ __forceinline__ float operator()(float f) const { return (float)((double)f * c); }
+};
 
-__device__ __forceinline__ uint4 scale_16(const uint4& v, const ClipCoef& c, __nv_bfloat16) {
+template <class S>
+__device__ __forceinline__ uint4 scale_16(const uint4& v, const S& c, __nv_bfloat16) {
   float f[8];
   bf16x8_to_f32(v, f);
-  return make_uint4(pack_bf16x2(scaled(f[0], c), scaled(f[1], c)), pack_bf16x2(scaled(f[2], c), scaled(f[3], c)),
-                    pack_bf16x2(scaled(f[4], c), scaled(f[5], c)), pack_bf16x2(scaled(f[6], c), scaled(f[7], c)));
+  return make_uint4(pack_bf16x2(c(f[0]), c(f[1])), pack_bf16x2(c(f[2]), c(f[3])),
+                    pack_bf16x2(c(f[4]), c(f[5])), pack_bf16x2(c(f[6]), c(f[7])));
 }
-__device__ __forceinline__ uint4 scale_16(const uint4& v, const ClipCoef& c, float) {
-  return make_uint4(__float_as_uint(scaled(__uint_as_float(v.x), c)), __float_as_uint(scaled(__uint_as_float(v.y), c)),
-                    __float_as_uint(scaled(__uint_as_float(v.z), c)), __float_as_uint(scaled(__uint_as_float(v.w), c)));
+template <class S>
+__device__ __forceinline__ uint4 scale_16(const uint4& v, const S& c, float) {
+  return make_uint4(__float_as_uint(c(__uint_as_float(v.x))), __float_as_uint(c(__uint_as_float(v.y))),
+                    __float_as_uint(c(__uint_as_float(v.z))), __float_as_uint(c(__uint_as_float(v.w))));
 }
 
 // dst = c src over n elements; 16-byte accesses where both sides have the same offset from a
 // 16-byte boundary.  src and dst are the same buffer or do not overlap.
-template <typename T>
-__device__ __forceinline__ void chunk_scale(const T* src, T* dst, int n, const ClipCoef& c) {
+template <typename T, class S>
+__device__ __forceinline__ void chunk_scale(const T* src, T* dst, int n, const S& c) {
   constexpr int V = 16 / sizeof(T);
   const int tid = threadIdx.x;
   auto one = [&](int i) {
-    const float f = scaled(clip_load1(src + i), c);
+    const float f = c(clip_load1(src + i));
     if constexpr (sizeof(T) == 2) dst[i] = __float2bfloat16_rn(f);
     else dst[i] = f;
   };
@@ -215,11 +226,8 @@ __device__ __forceinline__ void chunk_scale(const T* src, T* dst, int n, const C
 
 // The coefficient: 1 when the norm is within max_norm or not finite (the caller sees the norm
 // and skips the step; a NaN that spread to every gradient could not be told from its source).
-__device__ __forceinline__ ClipCoef clip_coef(double norm, double max_norm) {
-  if (!(norm > max_norm && norm < __longlong_as_double(0x7ff0000000000000LL))) return ClipCoef{1.0f, 0.0f};
-  const double c = max_norm / norm;
-  const float hi = (float)c;
-  return ClipCoef{hi, (float)(c - (double)hi)};
+__device__ __forceinline__ double clip_coef(double norm, double max_norm) {
+  return norm > max_norm && norm < __longlong_as_double(0x7ff0000000000000LL) ? max_norm / norm : 1.0;
 }
 
 template <int N>
@@ -229,21 +237,26 @@ grad_scale_kernel(const __grid_constant__ ClipTable<N> t, ClipScaleArgs a) {
   pdl_wait();
   const double norm = sqrt(total_of(a.sumsq, a.n_sums));
   if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
-  const ClipCoef coef = clip_coef(norm, a.max_norm);
+  const double coef = clip_coef(norm, a.max_norm);
   const int chunks = t.chunk0[t.n_tensors];
-  // last chunks first: they were read last and may still be in L2
-  for (int k = blockIdx.x; k < chunks; k += gridDim.x) {
-    const int c = chunks - 1 - k;
-    const int i = clip_tensor(t, c);
-    if (coef.hi == 1.0f && coef.lo == 0.0f && t.e[i].src == t.e[i].dst) continue;   // in place and nothing to scale
-    const int64_t off = (int64_t)(c - t.chunk0[i]) * kClipChunk;
-    const int64_t left = t.e[i].n - off;
-    const int n = left < kClipChunk ? (int)left : kClipChunk;
-    if (t.bf16[i >> 5] >> (i & 31) & 1u)
-      chunk_scale(static_cast<const __nv_bfloat16*>(t.e[i].src) + off, static_cast<__nv_bfloat16*>(t.e[i].dst) + off, n, coef);
-    else
-      chunk_scale(static_cast<const float*>(t.e[i].src) + off, static_cast<float*>(t.e[i].dst) + off, n, coef);
-  }
+  auto scale = [&](const auto& c) {
+    // last chunks first: they were read last and may still be in L2
+    for (int k = blockIdx.x; k < chunks; k += gridDim.x) {
+      const int i = clip_tensor(t, chunks - 1 - k);
+      if (coef == 1.0 && t.e[i].src == t.e[i].dst) continue;   // in place and nothing to scale
+      const int64_t off = (int64_t)(chunks - 1 - k - t.chunk0[i]) * kClipChunk;
+      const int64_t left = t.e[i].n - off;
+      const int n = left < kClipChunk ? (int)left : kClipChunk;
+      if (t.bf16[i >> 5] >> (i & 31) & 1u)
+        chunk_scale(static_cast<const __nv_bfloat16*>(t.e[i].src) + off, static_cast<__nv_bfloat16*>(t.e[i].dst) + off, n, c);
+      else
+        chunk_scale(static_cast<const float*>(t.e[i].src) + off, static_cast<float*>(t.e[i].dst) + off, n, c);
+    }
+  };
+  const float hi = (float)coef, lo = (float)(coef - (double)hi);
+  if (coef < 0x1p-100) scale(ScaleFp64{coef});
+  else if (lo == 0.0f) scale(ScaleFp32{hi});
+  else scale(ScaleTwoFp32{hi, lo});
 }
 
 }  // namespace moe

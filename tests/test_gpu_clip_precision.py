@@ -40,3 +40,22 @@ def test_scaled_gradients_are_rounded_once(dt, limit):
     outs = [torch.empty_like(b) for b in before]
     clip.scale_grads(before, torch.tensor([norm * norm], dtype=torch.float64, device="cuda"), limit, out=outs)
     check(outs)
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("std,limit", [(1e37, 1e-3), (1e37, 1e-12), (1e30, 1e-5), (3e36, 1e-35), (1e12, 1e-19)])
+def test_coefficients_below_the_fp32_range(dt, std, limit):
+    """A norm of 10^39 and more is 64-bit; so is its quotient, down to 10^-75."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    before = [(torch.randn(n, generator=gen, device="cuda") * std).to(dt) for n in (5000, 33)]
+    norm = math.sqrt(R.norm_sq(before))
+    assert all(bool(b.isfinite().all()) for b in before)
+    got = [b.clone() for b in before]
+    clip.clip_grad_norm(got, limit)
+    least = torch.finfo(dt).smallest_normal * torch.finfo(dt).eps   # a step below the normal range
+    for g, b in zip(got, before):
+        ref = b.double() * (limit / norm)
+        tol = 1.001 * R.E + (R.half(BF) if dt == BF else 0)
+        assert bool(((g.double() - ref).abs() <= tol * ref.abs() + least).all())
+    big = torch.cat([g.abs().double() for g in got]).max()
+    assert float(big) > 0.01 * limit    # ordinary values come out of it
