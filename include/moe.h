@@ -376,10 +376,11 @@ moe_status moe_block_norm_backward(const void* y, const void* r, const void* dr,
  * their type), element counts (0 allowed), MOE_FP32 or MOE_BF16 each; they are read during
  * the call only.  outs[i] is grads[i] itself (in place) or a buffer that overlaps none of the
  * others; the same buffer twice among the outputs is refused.  Squares, sums, N and max_norm / N
- * are 64-bit, the sums in an order fixed by the sizes.  When N <= max_norm, or N is not finite
- * (a gradient is not), the coefficient is 1: gradients in place stay untouched, and the caller
- * sees N (an fp32 norm reads infinite too when a finite N is past 2^128; the gradients are then
- * scaled by max_norm / N).  A scaled gradient is rounded to fp32 once, a bf16 one then to bf16.
+ * are 64-bit, the sums in an order fixed by the sizes, the buffers' offsets from 16 bytes and the
+ * GPU's SM count.  When N <= max_norm, or N is not finite (a gradient is not), the coefficient
+ * is 1: gradients in place stay untouched, and the caller sees N (an fp32 norm reads infinite too
+ * when a finite N is past 2^128; the gradients are then scaled by max_norm / N).  A scaled
+ * gradient is rounded to fp32 once, a bf16 one then to bf16.
  * workspace: 8-byte aligned DEVICE memory of moe_grad_workspace(n_tensors) bytes, free again when
  * the call's work is done.  sumsq, norm and the workspace may not overlap each other or a tensor.
  *   moe_clip_grad_norm  both steps; norm [1] fp32 (DEVICE) = N

@@ -6,7 +6,8 @@
 // so a call can be captured into a graph); each is cut into chunks, and the CTAs take chunks
 // round-robin, so a few huge tensors and thousands of tiny ones both fill the SMs.  Squares
 // and sums are 64-bit: a sum over 10^9 elements loses nothing, and gradients of 1e-30 or 1e30,
-// whose squares leave the fp32 range, count.  The order of the sums is fixed by the sizes.
+// whose squares leave the fp32 range, count.  The order of the sums is fixed by the sizes, the
+// buffers' offsets from 16 bytes and the SM count.
 //
 // Bound by HBM: the norm reads each gradient once (881 MB of fp32: 127 us, 6.9 TB/s), clipping reads
 // it again and writes it (2.28 GB: 1.09 ms, 6.3 TB/s over the three passes); the second pass runs

@@ -60,9 +60,11 @@ def clip_grad_norm(replicated, sharded, max_norm: float, group=None, sumsq_fn=No
 
     `replicated`: gradients every rank holds alike (data-parallel ones after their all-reduce;
     the router and the shared experts); `sharded`: those of this rank's own parameters (its
-    routed experts).  The norm counts the replicated ones once and every rank's sharded ones:
-    one all-reduce of a single fp64 sum.  Either list may be empty, not both.  Returns the norm
-    before, [1] fp32.
+    routed experts).  The norm counts the replicated ones once and every rank's sharded ones, by
+    one all-reduce of three fp64 values.  Every rank scales by the same total, bit for bit: the
+    replicated part is the mean of the ranks' sums, which may differ in their last bits (their
+    order depends on the buffers' alignment), so replicas stay alike.  Either list may be empty,
+    not both.  Returns the norm before, [1] fp32.
 
     `sumsq_fn(grads)` and `scale_fn(grads, sumsq, max_norm)` compute the sum of squares and scale;
     the defaults are the library's kernels (`clip.grad_sumsq`, `clip.scale_grads`)."""
@@ -73,9 +75,14 @@ def clip_grad_norm(replicated, sharded, max_norm: float, group=None, sumsq_fn=No
     if not replicated and not sharded:
         raise ValueError("no gradients")
     dev = (replicated or sharded)[0].device
-    # a rank without sharded gradients takes part in the all-reduce all the same
-    total = sumsq_fn(sharded) if sharded else torch.zeros(1, dtype=torch.float64, device=dev)
-    dist.all_reduce(total, group=group)
+    # sharded, replicated, ranks that hold replicated ones; a rank without either kind takes part
+    # in the all-reduce all the same
+    sums = torch.zeros(3, dtype=torch.float64, device=dev)
+    if sharded:
+        sums[:1] = sumsq_fn(sharded)
     if replicated:
-        total = total + sumsq_fn(replicated)
+        sums[1:2] = sumsq_fn(replicated)
+        sums[2] = 1.0
+    dist.all_reduce(sums, group=group)
+    total = sums[:1] + sums[1:2] / sums[2:].clamp(min=1.0)
     return scale_fn(replicated + sharded, total, max_norm)
