@@ -55,6 +55,13 @@ def global_balance_loss(layer, out, psum_buf: torch.Tensor, counts_buf: torch.Te
     return loss_fn(counts_buf, psum_buf, n_global, layer.alpha1, aux_buf)
 
 
+def _collective_device(group) -> torch.device:
+    """Where the tensors of the group's collectives lie."""
+    if "nccl" in dist.get_backend(group):
+        return torch.device("cuda", torch.cuda.current_device())
+    return torch.device("cpu")
+
+
 def clip_grad_norm(replicated, sharded, max_norm: float, group=None, sumsq_fn=None, scale_fn=None) -> torch.Tensor:
     """Clip one model's gradients over the ranks of `group` to `max_norm` together, in place.
 
@@ -63,8 +70,9 @@ def clip_grad_norm(replicated, sharded, max_norm: float, group=None, sumsq_fn=No
     routed experts).  The norm counts the replicated ones once and every rank's sharded ones, by
     one all-reduce of three fp64 values.  Every rank scales by the same total, bit for bit: the
     replicated part is the mean of the ranks' sums, which may differ in their last bits (their
-    order depends on the buffers' alignment), so replicas stay alike.  Either list may be empty,
-    not both.  Returns the norm before, [1] fp32.
+    order depends on the buffers' alignment), so replicas stay alike.  Either list may be empty; a
+    rank with neither kind still takes part, since the others wait for it.  Returns the norm
+    before, [1] fp32.
 
     `sumsq_fn(grads)` and `scale_fn(grads, sumsq, max_norm)` compute the sum of squares and scale;
     the defaults are the library's kernels (`clip.grad_sumsq`, `clip.scale_grads`)."""
@@ -72,9 +80,10 @@ def clip_grad_norm(replicated, sharded, max_norm: float, group=None, sumsq_fn=No
         from . import clip
         sumsq_fn, scale_fn = sumsq_fn or clip.grad_sumsq, scale_fn or clip.scale_grads
     replicated, sharded = list(replicated), list(sharded)
-    if not replicated and not sharded:
+    none = not replicated and not sharded
+    if none and not dist.is_initialized():
         raise ValueError("no gradients")
-    dev = (replicated or sharded)[0].device
+    dev = _collective_device(group) if none else (replicated or sharded)[0].device
     # sharded, replicated, ranks that hold replicated ones; a rank without either kind takes part
     # in the all-reduce all the same
     sums = torch.zeros(3, dtype=torch.float64, device=dev)
@@ -85,4 +94,6 @@ def clip_grad_norm(replicated, sharded, max_norm: float, group=None, sumsq_fn=No
         sums[2] = 1.0
     dist.all_reduce(sums, group=group)
     total = sums[:1] + sums[1:2] / sums[2:].clamp(min=1.0)
+    if none:
+        return total.sqrt().float()
     return scale_fn(replicated + sharded, total, max_norm)

@@ -62,3 +62,23 @@ def test_every_rank_scales_by_the_same_total(world):
     shared = float((torch.arange(1.0, 6.0) / 3).double().square().sum())
     for total, want in zip(got[0], (own + shared, own, own + shared)):
         assert total == pytest.approx(want, rel=1e-14)
+
+
+def _one_without(rank):
+    def sumsq(ts):
+        return sum(t.double().square().sum() for t in ts).reshape(1)
+
+    def scale(ts, total, max_norm):
+        return total.sqrt().float()
+
+    own = [torch.full((3,), 2.0)] if rank == 0 else []
+    first = parallel.clip_grad_norm([], own, 1.0, sumsq_fn=sumsq, scale_fn=scale)
+    nobody = parallel.clip_grad_norm([], [], 1.0, sumsq_fn=sumsq, scale_fn=scale)
+    after = torch.ones(1)
+    dist.all_reduce(after)      # the ranks' collectives still belong together
+    return float(first), first.dtype == torch.float32, float(nobody), float(after)
+
+
+def test_a_rank_without_gradients_takes_part():
+    got = _run(_one_without, 2)
+    assert got[0] == got[1] == (pytest.approx(12.0 ** 0.5, rel=1e-7), True, 0.0, 2.0)
