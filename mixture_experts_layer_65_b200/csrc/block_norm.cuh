@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), MAXT == 160 ? 3 : MAXT
       if (a.w_post || a.gate_kind == kGateToken) {   // the same for every thread
         mean = row_sum<kWarpRow>(vsum(sum), red[odd][1]);
         if (a.gate_kind == kGateToken && tid == 0) a.d_gate_tok[row] = mean;
-        mean = a.w_post ? mean * inv_d : 0.f;
+        mean *= inv_d;
       }
       float m[V];
       vset(k, s_post * gt);
@@ -669,7 +669,8 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), MAXT == 160 ? 3 : MAXT
             vmul(y[kHolds ? i : 0], y[kHolds ? i : 0], ks);
           }
           vmul(g[i], g[i], k);
-          vfma(g[i], y[kHolds ? i : 0], m, g[i]);
+          // (without a norm y has no part in dy, and 0 times an infinite y would be NaN)
+          if (a.w_post) vfma(g[i], y[kHolds ? i : 0], m, g[i]);
           store_row<T, V, SHIFT>(a.dy, base, col(i), a.d, g[i]);
         }
     }
