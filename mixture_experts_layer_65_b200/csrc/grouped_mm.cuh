@@ -104,12 +104,28 @@ __device__ __forceinline__ int group_of(const GroupTable& t, int G, int tile) {
   return lo;
 }
 
+// Tiles of bm x bn at most (every expert with rows has one ragged tile row).
+__host__ __device__ constexpr int64_t grouped_tiles(int op, int64_t G, int64_t rows, int64_t n, int64_t k, int bm,
+                                                    int bn) {
+  const int64_t nt = ((op == kGroupedMM ? n : k) + bn - 1) / bn;
+  return op == kGroupedWgrad ? G * nt * ((n + bm - 1) / bm) : ((rows + bm - 1) / bm + (G < rows ? G : rows)) * nt;
+}
+
 // Parts of each expert's rows in a weight gradient of `tiles` tiles whose kernel has room for
 // `slots`: as many as fit, of at least `least` rows on average, 256 at most.
 __host__ __device__ constexpr int wgrad_splits(int64_t rows, int G, int64_t tiles, int slots, int least) {
   const int64_t fill = slots / tiles, rest = rows / G / least;
   const int64_t s = fill < rest ? fill : rest;
   return s < 1 ? 1 : s > 256 ? 256 : (int)s;
+}
+// The same by the shape: for the tensor cores' kernel of 256 x 256 tiles (`tma`), or the others'
+// smaller ones.  (Slots are those of a B200's 148 SMs, so that the workspace's size needs no device.)
+// One expert of 100,000 rows, 64 x 64: 28 us in 74 parts, 0.5 ms in one; 72 tiles for 74 slots stay
+// whole (split in two, 796 us against 478 for 65,536 rows).
+__host__ __device__ constexpr int wgrad_parts(int G, int64_t rows, int n, int k, bool tma) {
+  constexpr int kSms = 148;
+  return tma ? wgrad_splits(rows, G, grouped_tiles(kGroupedWgrad, G, rows, n, k, 256, 256), kSms / 2, 1024)
+             : wgrad_splits(rows, G, grouped_tiles(kGroupedWgrad, G, rows, n, k, 64, 64), 4 * kSms, 512);
 }
 // Part s of an expert's rows: whole MMA steps of 16 rows but for the last part.
 __host__ __device__ inline void split_rows(int& row0, int& rows, int splits, int s) {
@@ -186,6 +202,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 constexpr bool simt_sums_shared(int bm) { return bm == 128; }
 constexpr size_t simt_smem_bytes(int bm, int bn) {
   return simt_sums_shared(bm) ? (size_t)bm * bn * sizeof(float) : 0;
+}
+// The tiles' side: the largest that gives every SM two CTAs of 128 x 128 or three of 64 x 64; small
+// problems take 32 x 32 with the contraction over four sets of threads (one expert of 384 rows,
+// 1024 x 1024: 68 us -> 45) and one element a load (16-byte loads turned into K-major rows of so
+// small a tile cost more than they save: 60 experts of 25 rows, 200 x 332, 27 us against 41; on
+// larger tiles they save: 4 experts of 500 rows, 1000 x 1000, 126 us against 155).
+__host__ __device__ constexpr int simt_tile(int64_t tiles128, int64_t tiles64, int n_sms) {
+  return tiles128 >= 2 * n_sms ? 128 : tiles64 >= 3 * n_sms ? 64 : 32;
 }
 template <int OP, int BM, int BN, int R, int V, int KS>
 __global__ void __launch_bounds__(BM * BN / (R * R) * KS, KS > 1 || simt_sums_shared(BM) ? 2 : 1)

@@ -22,6 +22,9 @@ namespace moe {
 constexpr int kGwpBK = 32;
 constexpr int kGwpChunk = 15;   // steps per accumulator chain of a weight gradient: 480 rows
 
+// The tiles' side: 64 where 128 x 128 would not give every SM a tile.
+__host__ __device__ constexpr int warp_tile(int64_t tiles128, int n_sms) { return tiles128 >= n_sms ? 128 : 64; }
+
 struct GroupedWarpArgs {
   const __nv_bfloat16* a;   // mm: x, dgrad: dy, wgrad: dy
   const __nv_bfloat16* b;   // mm, dgrad: W, wgrad: x

@@ -54,6 +54,7 @@ constexpr int kGwThreads = 64 + 32 * (kGpEpiWarps + 2);    // + the zeroing and 
 constexpr int kGwSlots = 4;                                // answers, and tiles handed on
 constexpr int kGwAhead = 2;                                // requests made ahead
 constexpr size_t kGwSmemBytes = 1024 + kGwStages * kGwStageBytes + 1024;
+static_assert(kPairBM == 256 && kGemmBN == 256, "wgrad_parts counts tiles of 256 x 256");
 static_assert(kGwBox % 1024 == 0 && kGwRows % 16 == 0, "swizzle atoms, MMA steps");
 
 struct GroupedWgradArgs {

@@ -35,19 +35,10 @@ moe_status check_shape(const Shape& s) {
   return MOE_OK;
 }
 
-// Tiles of bm x bn at most (every expert with rows has one ragged tile row).
 template <int OP>
-int64_t tiles_of(const Shape& s, int bm, int bn) {
-  const int64_t nt = ((OP == kGroupedMM ? s.n : s.k) + bn - 1) / bn;
-  return OP == kGroupedWgrad ? s.G * nt * ((s.n + bm - 1) / bm)
-                             : ((s.rows + bm - 1) / bm + (s.G < s.rows ? s.G : s.rows)) * nt;
-}
+int64_t tiles_of(const Shape& s, int bm, int bn) { return grouped_tiles(OP, s.G, s.rows, s.n, s.k, bm, bn); }
 
-// fp32.  The largest tiles that give every SM two CTAs of 128 x 128 or three of 64 x 64; small
-// problems take 32 x 32 with the contraction over four sets of threads (one expert of 384 rows,
-// 1024 x 1024: 68 us -> 45) and one element a load (16-byte loads turned into K-major rows of so
-// small a tile cost more than they save: 60 experts of 25 rows, 200 x 332, 27 us against 41; on
-// larger tiles they save: 4 experts of 500 rows, 1000 x 1000, 126 us against 155).
+// fp32 (simt_tile).
 template <int OP, int BM, int BN, int R, int V, int KS>
 cudaError_t launch_simt_tile(const GroupedSimtArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
   constexpr int kThreads = BM * BN / (R * R) * KS;
@@ -68,19 +59,21 @@ cudaError_t launch_simt_tile(const GroupedSimtArgs& a, const Shape& s, int n_sms
 template <int OP>
 cudaError_t launch_simt(const GroupedSimtArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
   const bool v4 = s.n % 4 == 0 && s.k % 4 == 0 && aligned16(a.a) && aligned16(a.b);
-  if (a.splits * tiles_of<OP>(s, 128, 128) >= 2 * n_sms)
-    return v4 ? launch_simt_tile<OP, 128, 128, 8, 4, 1>(a, s, n_sms, st)
-              : launch_simt_tile<OP, 128, 128, 8, 1, 1>(a, s, n_sms, st);
-  if (a.splits * tiles_of<OP>(s, 64, 64) >= 3 * n_sms)
-    return v4 ? launch_simt_tile<OP, 64, 64, 8, 4, 1>(a, s, n_sms, st)
-              : launch_simt_tile<OP, 64, 64, 8, 1, 1>(a, s, n_sms, st);
-  return launch_simt_tile<OP, 32, 32, 4, 1, 4>(a, s, n_sms, st);
+  switch (simt_tile(a.splits * tiles_of<OP>(s, 128, 128), a.splits * tiles_of<OP>(s, 64, 64), n_sms)) {
+    case 128:
+      return v4 ? launch_simt_tile<OP, 128, 128, 8, 4, 1>(a, s, n_sms, st)
+                : launch_simt_tile<OP, 128, 128, 8, 1, 1>(a, s, n_sms, st);
+    case 64:
+      return v4 ? launch_simt_tile<OP, 64, 64, 8, 4, 1>(a, s, n_sms, st)
+                : launch_simt_tile<OP, 64, 64, 8, 1, 1>(a, s, n_sms, st);
+    default:
+      return launch_simt_tile<OP, 32, 32, 4, 1, 4>(a, s, n_sms, st);
+  }
 }
 
-// bf16 that TMA cannot take: 64 x 64 tiles where 128 x 128 would not give every SM one.  Weight
-// gradients, which keep two sets of sums, have an SM's registers for one CTA of the larger tiles
-// (64 experts of 5 rows, 515 x 1027: 102 us, two that spill 131; one of 5000 rows, 777 x 1313: 189
-// against 175).
+// bf16 that TMA cannot take (warp_tile).  Weight gradients, which keep two sets of sums, have an SM's
+// registers for one CTA of the larger tiles (64 experts of 5 rows, 515 x 1027: 102 us, two that
+// spill 131; one of 5000 rows, 777 x 1313: 189 against 175).
 template <int OP, int BM, int BN, int WM, int WN>
 cudaError_t launch_warp_tile(const GroupedWarpArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
   constexpr int kThreads = (BM / WM) * (BN / WN) * 32;
@@ -91,7 +84,8 @@ cudaError_t launch_warp_tile(const GroupedWarpArgs& a, const Shape& s, int n_sms
 }
 template <int OP>
 cudaError_t launch_warp(const GroupedWarpArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
-  if (a.splits * tiles_of<OP>(s, 128, 128) >= n_sms) return launch_warp_tile<OP, 128, 128, 64, 32>(a, s, n_sms, st);
+  if (warp_tile(a.splits * tiles_of<OP>(s, 128, 128), n_sms) == 128)
+    return launch_warp_tile<OP, 128, 128, 64, 32>(a, s, n_sms, st);
   return launch_warp_tile<OP, 64, 64, 32, 32>(a, s, n_sms, st);
 }
 
@@ -158,15 +152,7 @@ bool takes_tma(const Shape& s, const void* a, const void* b, const void* out) {
          aligned16(out);
 }
 
-// Parts of a weight gradient's rows: by the tiles of the kernel that runs it.  (Slots are those of
-// a B200's 148 SMs, so that the workspace's size needs no device.)  One expert of 100,000 rows,
-// 64 x 64: 28 us in 74 parts, 0.5 ms in one; 72 tiles for 74 slots stay whole (split in two,
-// 796 us against 478 for 65,536 rows).
-int splits_of(const Shape& s, bool tma) {
-  constexpr int kSms = 148;
-  if (tma) return wgrad_splits(s.rows, s.G, tiles_of<kGroupedWgrad>(s, kPairBM, kGemmBN), kSms / 2, 1024);
-  return wgrad_splits(s.rows, s.G, tiles_of<kGroupedWgrad>(s, 64, 64), 4 * kSms, 512);
-}
+int splits_of(const Shape& s, bool tma) { return wgrad_parts(s.G, s.rows, s.n, s.k, tma); }
 
 template <int OP>
 moe_status product(const void* a, const void* b, const int32_t* counts, const Shape& s, int accumulate,
