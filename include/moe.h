@@ -305,7 +305,8 @@ void moe_ep_destroy(moe_ep_handle* handle);
  *                         dw_e    += dy_e^T x_e with accumulate != 0 (the product rounded to
  *                         fp32, then the sum; a subnormal sum may become 0)
  * x, dx [rows, k]; y, dy [rows, n]; w [n_groups, n, k]; dw [n_groups, n, k] fp32; the rest in
- * dtype (MOE_BF16 or MOE_FP32), products accumulated in fp32 and rounded once.
+ * dtype (MOE_BF16 or MOE_FP32), products accumulated in fp32 and rounded once (long sums in pieces
+ * that are added up apart, whatever the length).
  * counts [n_groups] int32; all pointers DEVICE.  rows is the buffers' capacity: rows behind
  * the last expert's are not read into any result and not written; a negative count counts as
  * 0, and rows that counts claims past `rows` are ignored.  1 <= n_groups <= 1024, rows < 2^28

@@ -44,6 +44,13 @@ __host__ __device__ constexpr int gr_stages(int tile_rows) {
              ? kGrMaxStages
              : (int)(kGrRingBytes / gr_stage_bytes(tile_rows));
 }
+// k-blocks of one accumulator chain.  The tensor cores truncate when they add to an accumulator: a
+// chain of c values of one sign ends up to 6e-9 c below their sum (measured: 6e-3 of it at 2^20
+// values, where bf16's own half step is 4e-3).  Up to 16,384 values that is a fortieth of the half
+// step and one chain; longer contractions are cut, and the epilogue warps add the pieces in
+// registers, rounding to nearest.
+constexpr int kGrChain = 256;
+
 constexpr size_t kGrSmemBytes = 1024 + kGrRingBytes + 1024 + kGpEpiWarps * kGrTurnBytes;
 
 struct GroupedRowsArgs {
@@ -53,8 +60,9 @@ struct GroupedRowsArgs {
   int tile_rows;         // gr_tile_rows
 };
 
-// mm: W's rows are the output columns (K-major); dgrad: W's columns are (MN-major).
-template <int OP>
+// mm: W's rows are the output columns (K-major); dgrad: W's columns are (MN-major).  LONG: the
+// contraction has more than kGrChain k-blocks.
+template <int OP, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGpThreads, 1)
 grouped_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     GroupedRowsArgs a) {
@@ -180,32 +188,36 @@ grouped_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
       uint32_t phase = 0;
       bool ok = true;
       const uint32_t row_bytes = (uint32_t)(RT / 2) * 128u;
-      for (int tile = cid; tile < total && ok; tile += ncl, ++it) {
+      const int chain = LONG ? kGrChain : kbn;
+      for (int tile = cid; tile < total && ok; tile += ncl) {
         const Tile t = tile_of(tile, g);
         const uint32_t idesc = idesc_bf16_f32(kPairBM, mma_n(t)) | (kAMn ? kIdescAMn : 0u);
-        const int acc = it & 1;
-        ok = mbar_wait(smem_u32(&acc_empty[acc]), ((it >> 1) & 1) ^ 1u, abort_flag, err, kErrWaitMma);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t dt = tmem_base + static_cast<uint32_t>(acc * RT);
-        for (int kb0 = 0; kb0 < kbn; kb0 += kGemmKPS) {
-          ok = mbar_wait(smem_u32(&full[stage]), phase, abort_flag, err, kErrWaitMma);
+        for (int kc = 0; kc < kbn && ok; kc += chain, ++it) {
+          const int kend = kbn - kc < chain ? kbn : kc + chain;
+          const int acc = it & 1;
+          ok = mbar_wait(smem_u32(&acc_empty[acc]), ((it >> 1) & 1) ^ 1u, abort_flag, err, kErrWaitMma);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(base + (size_t)stage * stage_bytes);
-          const int nk = kbn - kb0 < kGemmKPS ? kbn - kb0 : kGemmKPS;
-          for (int j = 0; j < nk; ++j) {
-            const uint64_t ad = kAMn ? sdesc_mn_sw128(sa + j * (kGemmBK * 128u), kGrWBox)
-                                     : sdesc_k_sw128(sa + j * kGemmABytes);
-            const uint64_t bd = sdesc_k_sw128(sa + kGrABytes + j * row_bytes);
+          const uint32_t dt = tmem_base + static_cast<uint32_t>(acc * RT);
+          for (int kb0 = kc; kb0 < kend; kb0 += kGemmKPS) {
+            ok = mbar_wait(smem_u32(&full[stage]), phase, abort_flag, err, kErrWaitMma);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sa = smem_u32(base + (size_t)stage * stage_bytes);
+            const int nk = kend - kb0 < kGemmKPS ? kend - kb0 : kGemmKPS;
+            for (int j = 0; j < nk; ++j) {
+              const uint64_t ad = kAMn ? sdesc_mn_sw128(sa + j * (kGemmBK * 128u), kGrWBox)
+                                       : sdesc_k_sw128(sa + j * kGemmABytes);
+              const uint64_t bd = sdesc_k_sw128(sa + kGrABytes + j * row_bytes);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)   // 16 contraction values a step
-              tc_mma_f16_pair(dt, ad + (kAMn ? 128u : 2u) * k, bd + 2u * k, idesc, (kb0 | j | k) != 0);
+              for (int k = 0; k < 4; ++k)   // 16 contraction values a step
+                tc_mma_f16_pair(dt, ad + (kAMn ? 128u : 2u) * k, bd + 2u * k, idesc, ((kb0 - kc) | j | k) != 0);
+            }
+            tc_commit_pair_mc(smem_u32(&empty[stage]), 0x3);
+            if (++stage == S) { stage = 0; phase ^= 1u; }
           }
-          tc_commit_pair_mc(smem_u32(&empty[stage]), 0x3);
-          if (++stage == S) { stage = 0; phase ^= 1u; }
+          if (ok) tc_commit_pair_mc(smem_u32(&acc_full[acc]), 0x3);
         }
-        if (ok) tc_commit_pair_mc(smem_u32(&acc_full[acc]), 0x3);
       }
       tc_commit_pair_mc(smem_u32(drain), 0x3);
     }
@@ -216,21 +228,26 @@ grouped_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
     const int half = (warp - 2) >> 2;       // even or odd blocks of 32 rows
     uint8_t* turn = turn_base + (warp - 2) * kGrTurnBytes;
     int g = 0, it = 0;
-    for (int tile = cid; tile < total; tile += ncl, ++it) {
+    for (int tile = cid; tile < total; tile += ncl) {
       const Tile t = tile_of(tile, g);
-      const int acc = it & 1;
-      int ok = 1;
-      if (lane == 0) ok = mbar_wait(smem_u32(&acc_full[acc]), (it >> 1) & 1, abort_flag, err, kErrWaitEpilogue);
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      tc_fence_after();
-      const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * RT);
       const int col0 = t.n * kPairBM + (int)rank * 128 + q * 32;   // this warp's output columns
       const int col = col0 + (lane & 3) * 8;                       // this lane's when it stores
-      for (int rb = half * 32; rb < t.rows && col0 < out_cols; rb += 64) {
-        uint32_t v[32];
+      uint32_t tq;
+      auto ready = [&] {   // the next accumulator is full
+        int ok = 1;
+        if (lane == 0) ok = mbar_wait(smem_u32(&acc_full[it & 1]), (it >> 1) & 1, abort_flag, err, kErrWaitEpilogue);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+        tc_fence_after();
+        tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>((it & 1) * RT);
+        return true;
+      };
+      auto release = [&] {
+        tc_fence_before();
         __syncwarp();
-        tmem_ld32(tq + static_cast<uint32_t>(rb), v);
-        tmem_ld_wait(v);
+        if (lane == 0) mbar_arrive_relaxed_cluster(mapa_shared(smem_u32(&acc_empty[it & 1]), 0));
+        ++it;
+      };
+      auto store = [&](int rb, const uint32_t (&v)[32]) {   // 32 rows of this warp's columns
 #pragma unroll
         for (int i = 0; i < 32; ++i)   // row i, column lane
           *reinterpret_cast<__nv_bfloat16*>(turn + i * 64 + lane * 2) = __float2bfloat16_rn(__uint_as_float(v[i]));
@@ -245,10 +262,53 @@ grouped_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
           if (r < t.rows && col < out_cols)   // (out_cols is a multiple of 8)
             *reinterpret_cast<uint4*>(a.out + (size_t)(t.row + r) * out_cols + col) = w[i];
         }
+      };
+      if constexpr (LONG) {
+        uint32_t s[4][32] = {};
+        int ok = 1;
+        for (int kc = 0; kc < kbn; kc += kGrChain) {
+          ok = ready();
+          if (!ok) break;
+          const int blocks = RT / 64;   // of this warp: one or four (rows behind the tile's are not stored)
+          if (kc == 0) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (x < blocks) tmem_ld32(tq + static_cast<uint32_t>(half * 32 + 64 * x), s[x]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) tmem_ld_wait(s[x]);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (x < blocks) {
+                uint32_t v[32];
+                tmem_ld32(tq + static_cast<uint32_t>(half * 32 + 64 * x), v);
+                tmem_ld_wait(v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  s[x][i] = __float_as_uint(__fadd_rn(__uint_as_float(s[x][i]), __uint_as_float(v[i])));
+              }
+          }
+          release();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (half * 32 + 64 * x < t.rows && col0 < out_cols) {
+            __syncwarp();
+            store(half * 32 + 64 * x, s[x]);
+          }
+      } else {
+        if (!ready()) break;
+#pragma unroll 1
+        for (int rb = half * 32; rb < t.rows && col0 < out_cols; rb += 64) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld32(tq + static_cast<uint32_t>(rb), v);
+          tmem_ld_wait(v);
+          store(rb, v);
+        }
+        release();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_relaxed_cluster(mapa_shared(smem_u32(&acc_empty[acc]), 0));
     }
   }
 

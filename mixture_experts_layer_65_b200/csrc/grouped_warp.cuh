@@ -7,7 +7,8 @@
 // computed).  An operand whose contraction index is contiguous lies as [output][contraction],
 // one whose output index is as [contraction][output], read with ldmatrix and ldmatrix.trans
 // (16-byte chunks swizzled, or rows padded by 16 bytes, so that the reads do not meet in a bank).
-// wgrad adds up its accumulators in registers every kGwpChunk steps (see grouped_wgrad.cuh).
+// wgrad, and mm and dgrad with long contractions, add up their accumulators in registers every
+// kGwpChunk steps (see grouped_wgrad.cuh, kGrChain in grouped_rows.cuh).
 //
 // 8 experts of 1000 rows, 1001 x 2003: mm 279 us, dgrad 295, wgrad 283 (109 to 115 TFLOP/s; loaded
 // element by element 465, 358, 478; the FMA kernel 1210, 970, 1063).  Bound by the traffic between
@@ -20,7 +21,8 @@
 namespace moe {
 
 constexpr int kGwpBK = 32;
-constexpr int kGwpChunk = 15;   // steps per accumulator chain of a weight gradient: 480 rows
+constexpr int kGwpChunk = 15;     // steps per accumulator chain of a weight gradient: 480 rows
+constexpr int kGwpOneChain = 512;   // most steps of an uncut chain of mm and dgrad: 16,384 values
 
 // The tiles' side: 64 where 128 x 128 would not give every SM a tile.
 __host__ __device__ constexpr int warp_tile(int64_t tiles128, int n_sms) { return tiles128 >= n_sms ? 128 : 64; }
@@ -105,7 +107,8 @@ struct WarpUnit {
   }
 };
 
-template <int OP, int BM, int BN, int WM, int WN, int MINB>
+// CUT: accumulators are added up every kGwpChunk steps.
+template <int OP, int BM, int BN, int WM, int WN, int MINB, bool CUT>
 __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 32, MINB) grouped_warp_kernel(GroupedWarpArgs p) {
   constexpr int kThreads = (BM / WM) * (BN / WN) * 32;
   constexpr bool W = OP == kGroupedWgrad, kAMn = W, kBMn = OP != kGroupedMM;
@@ -177,7 +180,7 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 32, MINB) grouped_warp
         *reinterpret_cast<uint4*>(&Bs[buf][TB::at(o, q)]) = rb[l].aligned();
       }
     };
-    float acc[MI][NI][4], sum[W ? MI : 1][W ? NI : 1][4];
+    float acc[MI][NI][4], sum[CUT ? MI : 1][CUT ? NI : 1][4];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -185,7 +188,7 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 32, MINB) grouped_warp
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           acc[i][j][x] = 0.f;
-          if constexpr (W) sum[i][j][x] = 0.f;
+          if constexpr (CUT) sum[i][j][x] = 0.f;
         }
     if (Q > 0) {
       fetch(0);
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 32, MINB) grouped_warp
             }
           }
         }
-        if constexpr (W) {
+        if constexpr (CUT) {
           if (++step % kGwpChunk == 0) {
 #pragma unroll
             for (int i = 0; i < MI; ++i)
@@ -249,13 +252,14 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 32, MINB) grouped_warp
           const int m = m0 + wm + i * 16 + (lane >> 2) + (x >> 1) * 8;
           const int n = n0 + wn + j * 8 + (lane & 3) * 2 + (x & 1);
           if (m >= M || n >= out_cols) continue;
+          float v = acc[i][j][x];
+          if constexpr (CUT) v += sum[i][j][x];
           if constexpr (W) {
             if (Q == 0 && p.accumulate) continue;   // nothing to add: not touched
             float* o = static_cast<float*>(p.out) + (((size_t)part * p.G + g) * p.N + m) * p.K + n;
-            const float v = sum[i][j][x] + acc[i][j][x];
             *o = p.accumulate ? *o + v : v;
           } else {
-            static_cast<__nv_bfloat16*>(p.out)[(size_t)(grow0 + m) * out_cols + n] = __float2bfloat16_rn(acc[i][j][x]);
+            static_cast<__nv_bfloat16*>(p.out)[(size_t)(grow0 + m) * out_cols + n] = __float2bfloat16_rn(v);
           }
         }
   }

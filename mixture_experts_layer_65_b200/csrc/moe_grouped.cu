@@ -71,22 +71,28 @@ cudaError_t launch_simt(const GroupedSimtArgs& a, const Shape& s, int n_sms, cud
   }
 }
 
-// bf16 that TMA cannot take (warp_tile).  Weight gradients, which keep two sets of sums, have an SM's
-// registers for one CTA of the larger tiles (64 experts of 5 rows, 515 x 1027: 102 us, two that
+// bf16 that TMA cannot take (warp_tile).  Weight gradients and long contractions, which keep two sets
+// of sums, have an SM's registers for one CTA of the larger tiles (64 experts of 5 rows, 515 x 1027: 102 us, two that
 // spill 131; one of 5000 rows, 777 x 1313: 189 against 175).
-template <int OP, int BM, int BN, int WM, int WN>
+template <int OP, int BM, int BN, int WM, int WN, bool CUT>
 cudaError_t launch_warp_tile(const GroupedWarpArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
   constexpr int kThreads = (BM / WM) * (BN / WN) * 32;
-  constexpr int kCtas = (OP == kGroupedWgrad && BM == 128 ? 256 : 512) / kThreads;   // of an SM
+  constexpr int kCtas = (CUT && BM == 128 ? 256 : 512) / kThreads;   // of an SM
   const int64_t tiles = a.splits * tiles_of<OP>(s, BM, BN), most = (int64_t)n_sms * kCtas;
-  return launch_pdl(grouped_warp_kernel<OP, BM, BN, WM, WN, kCtas>, dim3((unsigned)(tiles < most ? tiles : most)),
+  return launch_pdl(grouped_warp_kernel<OP, BM, BN, WM, WN, kCtas, CUT>, dim3((unsigned)(tiles < most ? tiles : most)),
                     dim3(kThreads), 0, st, a);
+}
+template <int OP, bool CUT>
+cudaError_t launch_warp_cut(const GroupedWarpArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
+  if (warp_tile(a.splits * tiles_of<OP>(s, 128, 128), n_sms) == 128)
+    return launch_warp_tile<OP, 128, 128, 64, 32, CUT>(a, s, n_sms, st);
+  return launch_warp_tile<OP, 64, 64, 32, 32, CUT>(a, s, n_sms, st);
 }
 template <int OP>
 cudaError_t launch_warp(const GroupedWarpArgs& a, const Shape& s, int n_sms, cudaStream_t st) {
-  if (warp_tile(a.splits * tiles_of<OP>(s, 128, 128), n_sms) == 128)
-    return launch_warp_tile<OP, 128, 128, 64, 32>(a, s, n_sms, st);
-  return launch_warp_tile<OP, 64, 64, 32, 32>(a, s, n_sms, st);
+  if constexpr (OP != kGroupedWgrad)
+    if ((OP == kGroupedMM ? s.k : s.n) <= kGwpOneChain * kGwpBK) return launch_warp_cut<OP, false>(a, s, n_sms, st);
+  return launch_warp_cut<OP, true>(a, s, n_sms, st);
 }
 
 // Clusters of `kernel` that can be resident at once on the current device (asked for once per
@@ -118,30 +124,31 @@ moe_status pair_clusters(const void* kernel, int threads, size_t smem, std::atom
 template <int OP>
 moe_status launch_tc(const void* a, const void* b, const int32_t* counts, const Shape& s, int accumulate,
                      int splits, void* out, int device, int n_sms, cudaStream_t st) {
-  static std::atomic<int> kept[64];
+  static std::atomic<int> kept[2][64];   // of each of OP's kernels
   CUtensorMap tmA, tmB;
   int clusters = 0;
   if constexpr (OP == kGroupedWgrad) {
     if (!encode_2d(&tmA, a, s.n, s.rows, kGwRows) || !encode_2d(&tmB, b, s.k, s.rows, kGwRows))
       return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for a grouped product's operand");
-    MOE_TRY(pair_clusters((const void*)grouped_wgrad_kernel, kGwThreads, kGwSmemBytes, kept, device, n_sms, &clusters));
+    MOE_TRY(pair_clusters((const void*)grouped_wgrad_kernel, kGwThreads, kGwSmemBytes, kept[0], device, n_sms, &clusters));
     // a cluster per tile
     const int64_t tiles = splits * tiles_of<OP>(s, kPairBM, kGemmBN);
     GroupedWgradArgs p{counts, static_cast<float*>(out), s.G, (int)s.rows, s.n, s.k, accumulate, splits};
     MOE_CUDA(launch_pdl(grouped_wgrad_kernel, dim3(2 * (unsigned)tiles), dim3(kGwThreads), kGwSmemBytes, st, tmB,
                         tmA, p));
   } else {
+    const bool cut = (OP == kGroupedMM ? s.k : s.n) > kGrChain * kGemmBK;
+    const auto kernel = cut ? grouped_rows_kernel<OP, true> : grouped_rows_kernel<OP, false>;
     const int rt = gr_tile_rows(s.rows, s.G);
     if (!encode_2d(&tmA, a, OP == kGroupedMM ? s.k : s.n, s.rows, rt / 2) ||
         !encode_3d(&tmB, b, s.k, s.n, s.G, OP == kGroupedMM ? 128 : kGemmKPS * kGemmBK))
       return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for a grouped product's operand");
-    MOE_TRY(pair_clusters((const void*)grouped_rows_kernel<OP>, kGpThreads, kGrSmemBytes, kept, device, n_sms,
-                          &clusters));
+    MOE_TRY(pair_clusters((const void*)kernel, kGpThreads, kGrSmemBytes, kept[cut], device, n_sms, &clusters));
     // at most: every expert with rows has one ragged tile row
     const int64_t tiles = ((s.rows + rt - 1) / rt + (s.G < s.rows ? s.G : s.rows)) *
                           (((OP == kGroupedMM ? s.n : s.k) + kPairBM - 1) / kPairBM);
     GroupedRowsArgs p{counts, s.G, (int)s.rows, s.n, s.k, static_cast<__nv_bfloat16*>(out), rt};
-    MOE_CUDA(launch_pdl(grouped_rows_kernel<OP>, dim3(2 * (unsigned)(tiles < clusters ? tiles : clusters)),
+    MOE_CUDA(launch_pdl(kernel, dim3(2 * (unsigned)(tiles < clusters ? tiles : clusters)),
                         dim3(kGpThreads), kGrSmemBytes, st, tmB, tmA, p));
   }
   return MOE_OK;
