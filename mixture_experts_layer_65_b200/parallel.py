@@ -71,8 +71,9 @@ def clip_grad_norm(replicated, sharded, max_norm: float, group=None, sumsq_fn=No
     one all-reduce of three fp64 values.  Every rank scales by the same total, bit for bit: the
     replicated part is the mean of the ranks' sums, which may differ in their last bits (their
     order depends on the buffers' alignment), so replicas stay alike.  Either list may be empty; a
-    rank with neither kind still takes part, since the others wait for it.  Returns the norm
-    before, [1] fp32.
+    rank with neither kind still takes part, since the others wait for it.  So does one whose
+    gradients are refused: it raises behind the all-reduce, and the others get a norm of NaN,
+    which leaves their gradients as they are.  Returns the norm before, [1] fp32.
 
     `sumsq_fn(grads)` and `scale_fn(grads, sumsq, max_norm)` compute the sum of squares and scale;
     the defaults are the library's kernels (`clip.grad_sumsq`, `clip.scale_grads`)."""
@@ -83,16 +84,23 @@ def clip_grad_norm(replicated, sharded, max_norm: float, group=None, sumsq_fn=No
     none = not replicated and not sharded
     if none and not dist.is_initialized():
         raise ValueError("no gradients")
-    dev = _collective_device(group) if none else (replicated or sharded)[0].device
-    # sharded, replicated, ranks that hold replicated ones; a rank without either kind takes part
-    # in the all-reduce all the same
-    sums = torch.zeros(3, dtype=torch.float64, device=dev)
-    if sharded:
-        sums[:1] = sumsq_fn(sharded)
-    if replicated:
-        sums[1:2] = sumsq_fn(replicated)
-        sums[2] = 1.0
+    # sharded, replicated, ranks that hold replicated ones; a rank without either kind, or whose sums
+    # fail, takes part in the all-reduce all the same
+    error = None
+    try:
+        dev = _collective_device(group) if none else (replicated or sharded)[0].device
+        sums = torch.zeros(3, dtype=torch.float64, device=dev)
+        if sharded:
+            sums[:1] = sumsq_fn(sharded)
+        if replicated:
+            sums[1:2] = sumsq_fn(replicated)
+            sums[2] = 1.0
+    except Exception as e:
+        error = e
+        sums = torch.full((3,), float("nan"), dtype=torch.float64, device=_collective_device(group))
     dist.all_reduce(sums, group=group)
+    if error is not None:
+        raise error
     total = sums[:1] + sums[1:2] / sums[2:].clamp(min=1.0)
     if none:
         return total.sqrt().float()

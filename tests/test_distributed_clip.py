@@ -82,3 +82,33 @@ def _one_without(rank):
 def test_a_rank_without_gradients_takes_part():
     got = _run(_one_without, 2)
     assert got[0] == got[1] == (pytest.approx(12.0 ** 0.5, rel=1e-7), True, 0.0, 2.0)
+
+
+def _one_refused(rank):
+    scaled = []
+
+    def sumsq(ts):
+        if any(t.dtype == torch.int32 for t in ts):
+            raise ValueError("not a gradient")
+        return sum(t.double().square().sum() for t in ts).reshape(1)
+
+    def scale(ts, total, max_norm):
+        scaled.append(float(total))
+        return total.sqrt().float()
+
+    got = []
+    for own in ([torch.ones(3, dtype=torch.int32 if rank else torch.float32)], [None if rank else torch.ones(3)]):
+        try:
+            norm = parallel.clip_grad_norm([], own, 1.0, sumsq_fn=sumsq, scale_fn=scale)
+            got.append(str(float(norm)))
+        except (ValueError, AttributeError) as e:
+            got.append(type(e).__name__)
+    after = torch.ones(1)
+    dist.all_reduce(after)
+    return got, len(scaled), float(after)
+
+
+def test_a_rank_whose_gradients_are_refused_takes_part():
+    got = _run(_one_refused, 2)
+    assert got[0] == (["nan", "nan"], 2, 2.0)
+    assert got[1] == (["ValueError", "AttributeError"], 0, 2.0)
