@@ -691,7 +691,8 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), MAXT == 160 ? 3 : MAXT
   }
 }
 
-// Column totals of the partial sums, in a fixed order; the channel gate's gradient and the
+// Column totals of the partial sums, in a fixed order and 64 bits (in fp32 chains of
+// 19 + 32 they gave most of the error: 1001 x 333, d_pre off by 1.4e-7 of its norm, 5e-8 now); the channel gate's gradient and the
 // weight's after a block share one sum: d_gate = w_post S, d_post = gate S.
 struct NormReduceArgs {
   const float* part_pre;   // [parts, d] or nullptr
@@ -709,20 +710,21 @@ constexpr int kNormRedRows = 32;
 static __global__ void __launch_bounds__(32 * kNormRedRows) block_norm_reduce_kernel(NormReduceArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ float sh[kNormRedRows][33];
+  __shared__ double sh[kNormRedRows][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + tx;
   const float* part = blockIdx.y == 0 ? a.part_pre : a.part_s;
   if (!part) return;   // uniform over the CTA
-  float v = 0.f;
+  double sum = 0.0;
   if (c < a.d)
-    for (int p = ty; p < a.parts; p += kNormRedRows) v += part[(int64_t)p * a.d + c];
-  sh[ty][tx] = v;
+    for (int p = ty; p < a.parts; p += kNormRedRows) sum += (double)part[(int64_t)p * a.d + c];
+  sh[ty][tx] = sum;
   __syncthreads();
   if (ty != 0 || c >= a.d) return;
-  v = 0.f;
+  sum = 0.0;
 #pragma unroll
-  for (int q = 0; q < kNormRedRows; ++q) v += sh[q][tx];
+  for (int q = 0; q < kNormRedRows; ++q) sum += sh[q][tx];
+  const float v = (float)sum;
   if (blockIdx.y == 0) {
     a.d_pre[c] = v;
   } else {
