@@ -19,15 +19,15 @@
 // kept per CTA.  Rows of other widths than whole 16-byte accesses start anywhere: their accesses
 // still are the aligned ones that the row touches (SHIFT), the elements of neighbouring rows in the
 // first and the last masked; a CTA (a warp) takes rows that all start alike, so that a thread's
-// columns, its parameters and column sums stay its own.  Every sum and statistic is fp32.  u and
-// the statistic s(r) come from r before it is rounded to its type (one rounding less than reading
-// it back).
+// columns, its parameters and column sums stay its own.  Sums and statistics are fp32, the CTAs'
+// column sums added up in 64 bits.  u and the statistic s(r) come from r before it is rounded to its
+// type (one rounding less than reading it back).
 //
-// Bound by HBM: bf16, both norms and a channel gate, forward 6.2 TB/s at 32,768 x 4096 (173 us, 0.95
-// of the copy rate) and 5.7 at 16,384 x 2048 (47 us); backward 5.3 and 5.4 (303 and 75 us), where
-// two chained row sums and 20 instructions a value begin to show.  Odd widths are bound by those
-// instructions (1.2e8 elements of bf16, d = 2001: 208 us and 361, 4.6 and 4.0 TB/s; by single
-// elements 491 and 899), rows of 64 columns by their number (8 of 32 lanes read: 1.8 TB/s), rows
+// Bound by HBM: bf16, both norms and a channel gate, forward 6.2 TB/s at 32,768 x 4096 (174 us, 0.94
+// of the copy rate; 185 us with other buffers each time) and 5.8 at 16,384 x 2048 (46 us); backward
+// 5.3 and 5.2 to 5.3 (303 and 75 to 77 us), where two chained row sums and 20 instructions a value
+// begin to show.  Odd widths are bound by those instructions (1.2e8 elements of bf16, d = 2001: 210 us
+// and 365, 4.6 and 3.9 TB/s; by single elements 491 and 899), rows of 64 columns by their number (8 of 32 lanes read: 1.8 TB/s), rows
 // past 8192 columns by barriers of 1024 threads (3.4 and 1.9 TB/s).
 #pragma once
 
@@ -691,9 +691,9 @@ __global__ void __launch_bounds__(norm_max_threads(MAXT), MAXT == 160 ? 3 : MAXT
   }
 }
 
-// Column totals of the partial sums, in a fixed order and 64 bits (in fp32 chains of
-// 19 + 32 they gave most of the error: 1001 x 333, d_pre off by 1.4e-7 of its norm, 5e-8 now); the channel gate's gradient and the
-// weight's after a block share one sum: d_gate = w_post S, d_post = gate S.
+// Column totals of the partial sums, in a fixed order and 64 bits (in fp32 chains of 19 + 32 they
+// gave most of the error: 1001 x 333, d_pre off by 1.4e-7 of its norm, 5e-8 now); the channel
+// gate's gradient and the weight's after a block share one sum: d_gate = w_post S, d_post = gate S.
 struct NormReduceArgs {
   const float* part_pre;   // [parts, d] or nullptr
   const float* part_s;     // [parts, d] or nullptr

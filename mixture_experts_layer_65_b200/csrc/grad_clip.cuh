@@ -10,7 +10,7 @@
 // buffers' offsets from 16 bytes and the SM count.
 //
 // Bound by HBM: the norm reads each gradient once (881 MB of fp32: 127 us, 6.9 TB/s), clipping reads
-// it again and writes it (2.28 GB: 1.09 ms, 6.3 TB/s over the three passes); the second pass runs
+// it again and writes it (2.28 GB: 1.08 to 1.10 ms, 6.3 TB/s over the three passes); the second pass runs
 // backwards through the tensors, whose ends are still in L2.  Small sets are bound by launches
 // (600 tensors of 0.9 million elements: 11.5 us on the device).
 #pragma once

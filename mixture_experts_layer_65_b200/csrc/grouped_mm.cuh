@@ -165,8 +165,10 @@ __global__ void __launch_bounds__(256) wgrad_sum_kernel(const float* part, int s
 // registers while this one is computed).  V elements a load: 4 when the widths are multiples of 4
 // and the buffers 16-byte aligned, else 1.  Sums are cut into pieces of kGsChunk steps, added up
 // apart: one chain of 4096 additions is off by 1e-6 of the result, pieces by a third of that.
-// Bound by FMA issue on the larger tiles (16 experts of 500 rows, 512 x 512: 115 us, 36 TFLOP/s), by
-// latency on the smallest (15 of 26 rows, 128 x 256: 8.8 us).
+// On the larger tiles 35 to 40 of the FMA units' 74 TFLOP/s (16 experts of 500 rows, 512 x 512: 116
+// us; 4 of 2368, 1024 x 1024: 497 to 543; a library's batched product of equal sizes 45 to 61): a
+// contraction value costs a thread four 16-byte shared loads for 32 paired FMAs.  The smallest are
+// bound by latency (15 of 26 rows, 128 x 256: 9 to 10 us).
 constexpr int kGsBK = 16;
 constexpr int kGsChunk = 16;   // steps: 256 products
 

@@ -15,9 +15,10 @@
 // 2 or 4 bytes a lane straight from registers: the same time).
 //
 // Bound by the tensor cores, and by the power they draw, with many rows per expert (64 experts of
-// 1536 rows, 2816 x 2048: 0.76-0.84 ms, 1.35-1.48 PFLOP/s, tensor pipe 88% active; short
-// contractions pay the change of tiles: 63 of 910 rows, 896 x 1280, 117 us, 80%), by HBM with few
-// (64 of 6 rows: 117 us, 6.3 TB/s of weights).
+// 1536 rows, 2816 x 2048: 0.80 ms, 1.43 PFLOP/s, tensor pipe 88% active; 0.98 ms once a loop meets
+// the power cap; short contractions pay the change of tiles and the clusters' uneven share of ragged
+// tiles: 63 of 910 rows, 896 x 1280, 118 us, 80%), by HBM with few (64 of 6 rows: 117 us, 6.3 TB/s of
+// weights).
 #pragma once
 
 #include "grouped_tc.cuh"

@@ -10,7 +10,7 @@
 // wgrad, and mm and dgrad with long contractions, add up their accumulators in registers every
 // kGwpChunk steps (see grouped_wgrad.cuh, kGrChain in grouped_rows.cuh).
 //
-// 8 experts of 1000 rows, 1001 x 2003: mm 279 us, dgrad 295, wgrad 283 (109 to 115 TFLOP/s; loaded
+// 8 experts of 1000 rows, 1001 x 2003: mm 280 us, dgrad 296, wgrad 287 (108 to 115 TFLOP/s; loaded
 // element by element 465, 358, 478; the FMA kernel 1210, 970, 1063).  Bound by the traffic between
 // L1, registers and shared memory: most of a step's 64 wide loads touch eight lines each, and the
 // MMAs' operands pass shared memory twice.

@@ -31,11 +31,11 @@
 // nothing but ask (the leader's), read the answer and hand the tile on, worked out: in the
 // producer that took 2,400 cycles a tile, which the ring could not cover.
 //
-// Bound by the tensor cores with long sums (64 experts of 6144 rows, 1408 x 2048: 1.78 ms, 1.27
-// PFLOP/s).  With short ones (1 row: 144 us; 160 rows: 152) by the stores' way out of the SM: a
+// Bound by the tensor cores with long sums (64 experts of 6144 rows, 1408 x 2048: 1.84 ms, 1.23
+// PFLOP/s).  With short ones (1 row: 143 us; 160 rows: 152) by the stores' way out of the SM: a
 // line takes 3 cycles there, and every barrier, load and MMA instruction of the other warps
 // queues with them; stores that stay in L2 take as long, so it is not HBM (738 MB: 112 us).  In
-// between (768 rows: 293 us, 0.97 PFLOP/s; 254 without the stores) both count.  Readers that
+// between (768 rows: 297 us, 0.95 PFLOP/s; 254 without the stores) both count.  Readers that
 // look up four words instead of a tile number saved 15 us of the 1-row case; stores through
 // shared memory and TMA boxes of 8 rows take 220 us there.
 #pragma once
