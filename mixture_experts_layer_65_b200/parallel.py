@@ -86,7 +86,7 @@ def clip_grad_norm(replicated, sharded, max_norm: float, group=None, sumsq_fn=No
         raise ValueError("no gradients")
     # sharded, replicated, ranks that hold replicated ones; a rank without either kind, or whose sums
     # fail, takes part in the all-reduce all the same
-    error = None
+    dev = error = None
     try:
         dev = _collective_device(group) if none else (replicated or sharded)[0].device
         sums = torch.zeros(3, dtype=torch.float64, device=dev)
@@ -97,7 +97,7 @@ def clip_grad_norm(replicated, sharded, max_norm: float, group=None, sumsq_fn=No
             sums[2] = 1.0
     except Exception as e:
         error = e
-        sums = torch.full((3,), float("nan"), dtype=torch.float64, device=_collective_device(group))
+        sums = torch.full((3,), float("nan"), dtype=torch.float64, device=dev or _collective_device(group))
     dist.all_reduce(sums, group=group)
     if error is not None:
         raise error
